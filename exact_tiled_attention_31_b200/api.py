@@ -4,12 +4,14 @@ Two layers:
 
 * ``fa_*`` (every name in ``EXPORTS``: forward, packed forward, the
   backward and its three launches, the packed and allocation-free
-  backwards, dropout forward/backward, decode, status and error helpers):
+  backwards, dropout forward/backward, decode, rotary positions, the paged
+  cache and decode over it, status and error helpers):
   the C entry points under the same names, taking raw device pointers (ints)
   and sizes, returning the ``fa_status`` code (or a size).
 * ``forward``, ``forward_varlen``, ``backward``, ``backward_varlen``,
-  ``backward_noalloc``, ``decode``: tensor conveniences that check
-  shapes/dtypes, allocate outputs and workspace with torch unless given
+  ``backward_noalloc``, ``decode``, ``rope_freqs``, ``rope``,
+  ``rope_backward``, ``append_paged``, ``decode_paged``, ``decode_prefix``:
+  tensor conveniences that check shapes/dtypes, allocate outputs and workspace with torch unless given
   (device memory and streams are all torch provides) and raise ``FAError``
   on a non-zero status.
 
@@ -18,9 +20,11 @@ is no fallback.  If ``libfa.so`` is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -32,7 +36,13 @@ EXPORTS = ("fa_fwd", "fa_fwd_varlen", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd
            "fa_bwd_finish", "fa_bwd_noalloc", "fa_bwd_varlen_workspace_size", "fa_bwd_varlen", "fa_status_string",
            "fa_check_device_error", "fa_launch_count", "fa_selftest_timeout", "fa_decode_num_splits",
            "fa_decode_workspace_size", "fa_decode", "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_varlen_dropout",
-           "fa_bwd_varlen_dropout")
+           "fa_bwd_varlen_dropout", "fa_rope_freqs", "fa_rope", "fa_append_paged", "fa_decode_paged_workspace_size",
+           "fa_decode_paged", "fa_decode_prefix_workspace_size", "fa_decode_prefix")
+
+# fa_rope_scaling, and the layouts of the structs fa_rows and fa_pages of include/fa.h
+ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+_ROWS = struct.Struct("@Pqqqi4x")   # data; batch, head, row stride; heads
+_PAGES = struct.Struct("@PPqPqiiii")  # k, v; page stride; table, its stride; n_pages, page_size, heads, max_pages
 
 # Fixed scratch size of fa_bwd_noalloc (FA_BWD_NOALLOC_SCRATCH_BYTES in include/fa.h).
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -99,6 +109,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_bwd_varlen_dropout.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, i, f, u64,
                                           u64, vp, sz, vp]
     lib.fa_bwd_varlen_dropout.restype = i
+    d, i64 = ctypes.c_double, ctypes.c_longlong
+    lib.fa_rope_freqs.argtypes = [i, d, i, d, i, d, d, vp, vp]
+    lib.fa_rope_freqs.restype = i
+    lib.fa_rope.argtypes = [vp, vp, i, vp, i, i, f, i, vp, i64, vp, i, i, i, i, i, vp]
+    lib.fa_rope.restype = i
+    lib.fa_append_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, vp, i, i, f, vp, i, i, vp]
+    lib.fa_append_paged.restype = i
+    lib.fa_decode_paged_workspace_size.argtypes = [i, i, i, i]
+    lib.fa_decode_paged_workspace_size.restype = sz
+    lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, i, i, i, f, i, vp, sz, vp]
+    lib.fa_decode_paged.restype = i
+    lib.fa_decode_prefix_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_decode_prefix_workspace_size.restype = sz
+    lib.fa_decode_prefix.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, f, i, vp, sz, vp]
+    lib.fa_decode_prefix.restype = i
     lib.fa_launch_count.argtypes = []
     lib.fa_launch_count.restype = ctypes.c_uint64
     _lib = lib
@@ -195,6 +220,45 @@ def fa_decode(q, k_cache, v_cache, seq_lens, o, lse, B, Hq, Hkv, L_max, D, scale
               workspace_bytes, stream) -> int:
     return load_library().fa_decode(q, k_cache, v_cache, seq_lens, o, lse, B, Hq, Hkv, L_max, D, scale, dt, n_splits,
                                     workspace, workspace_bytes, stream)
+
+
+def fa_rope_freqs(rot_dim, base, scaling, factor, original_len, beta_fast, beta_slow, freqs, amp) -> int:
+    return load_library().fa_rope_freqs(rot_dim, base, scaling, factor, original_len, beta_fast, beta_slow, freqs, amp)
+
+
+def fa_rope(x, y, n, freqs, rot_dim, interleaved, amp, backward, positions, positions_stride, cu_seqlens, nseq, B, S,
+            D, dt, stream) -> int:
+    """``x`` and ``y``: the bytes of n ``fa_rows`` each (or a pointer to them)."""
+    return load_library().fa_rope(x, y, n, freqs, rot_dim, int(interleaved), amp, int(backward), positions,
+                                  positions_stride, cu_seqlens, nseq, B, S, D, dt, stream)
+
+
+def fa_append_paged(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim, interleaved, amp,
+                    positions, D, dt, stream) -> int:
+    """``k``, ``v``, ``q``, ``q_out``: the bytes of one ``fa_rows`` each, ``pages``: of an ``fa_pages``."""
+    return load_library().fa_append_paged(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim,
+                                          int(interleaved), amp, positions, D, dt, stream)
+
+
+def fa_decode_paged_workspace_size(B, Hq, Hkv, D) -> int:
+    return load_library().fa_decode_paged_workspace_size(B, Hq, Hkv, D)
+
+
+def fa_decode_paged(q, pages, seq_lens, o, lse, B, Hq, D, scale, dt, workspace, workspace_bytes, stream) -> int:
+    """``pages``: the bytes of an ``fa_pages`` (or a pointer to it)."""
+    return load_library().fa_decode_paged(q, pages, seq_lens, o, lse, B, Hq, D, scale, dt, workspace, workspace_bytes,
+                                          stream)
+
+
+def fa_decode_prefix_workspace_size(B, Hq, Hkv, prefix_len, D) -> int:
+    return load_library().fa_decode_prefix_workspace_size(B, Hq, Hkv, prefix_len, D)
+
+
+def fa_decode_prefix(q, pages, seq_lens, prefix_len, prefix_table, o, lse, B, Hq, D, scale, dt, workspace,
+                     workspace_bytes, stream) -> int:
+    """``pages``: the bytes of an ``fa_pages`` (or a pointer to it)."""
+    return load_library().fa_decode_prefix(q, pages, seq_lens, prefix_len, prefix_table, o, lse, B, Hq, D, scale, dt,
+                                           workspace, workspace_bytes, stream)
 
 
 def fa_status_string(status: int) -> str:
@@ -405,9 +469,337 @@ def decode(q, k_cache, v_cache, seq_lens, scale: float | None = None, n_splits: 
     return o, lse
 
 
+# ---- rotary positions and the paged cache
+
+def _same_device(first, *ts):
+    """Every given tensor on ``first``'s CUDA device; returns the device."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must share one device: {t.device} != {dev}")
+    return dev
+
+
+@contextlib.contextmanager
+def _place(device, stream):
+    """Make ``device`` current and, if a stream is given, that stream too, so
+    that what is allocated inside belongs to the stream the kernels run on.
+    Yields the raw stream."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            raw = int(stream)
+            stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _int32(t, what, shape=None):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must be a contiguous CUDA int32 tensor" + (f" of shape {list(shape)}" if shape else ""))
+    return t.data_ptr()
+
+
+def _strides(x, dims, out=False):
+    """The strides of ``dims`` of x (0 for dimensions of one element), rows contiguous."""
+    size, st = x.shape, x.stride()
+    if st[-1] != 1 and size[-1] > 1:
+        raise ValueError("rows must be contiguous in the last dimension")
+    got = []
+    for d in dims:
+        s = st[d] if size[d] > 1 else 0
+        if s % 8 or (out and s == 0 and size[d] > 1):
+            raise ValueError("strides must be multiples of 8 elements" + (" and not zero in an output" if out else ""))
+        got.append(s)
+    return got
+
+
+def _extent(x):
+    """The bytes from an empty-free tensor's first element to behind its last."""
+    return x.data_ptr(), x.data_ptr() + x.element_size() * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride())))
+
+
+def _check_rows_out(x, y, what):
+    """An output for the rows of ``x``: x itself, or apart from it."""
+    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise ValueError(f"{what}: shape {tuple(y.shape)} {y.dtype} does not match {tuple(x.shape)} {x.dtype}")
+    if y.numel() and (y.data_ptr() != x.data_ptr() or y.stride() != x.stride()):
+        (a, b), (c, d) = _extent(x), _extent(y)
+        if a < d and c < b:
+            raise ValueError(f"{what} overlaps its input without being it")
+
+
+def _check_freqs(freqs, D):
+    import torch
+    if freqs.dtype != torch.float64 or not freqs.is_cuda or not freqs.is_contiguous() or freqs.dim() != 1:
+        raise ValueError("freqs must be a contiguous CUDA float64 tensor of rot_dim / 2 radians per position")
+    return 2 * freqs.shape[0]
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """The frequencies of ``rope`` and ``append_paged``: a float64 tensor of
+    rot_dim / 2 radians per position, and the factor ``amp`` to pass with it.
+    ``scaling``: None, "linear" (positions divided by ``factor``), "ntk" (a
+    larger base) or "yarn" (by parts; takes ``original_len``)."""
+    import torch
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
+    out = (ctypes.c_double * max(int(rot_dim) // 2, 1))()
+    amp = ctypes.c_float()
+    st = fa_rope_freqs(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor), int(original_len),
+                       float(beta_fast), float(beta_slow), out, ctypes.byref(amp))
+    if st != FA_OK:
+        raise FAError(st, "fa_rope_freqs")
+    return torch.tensor(list(out), dtype=torch.float64).to(device), amp.value
+
+
+def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, backward):
+    import torch
+    xs = (q,) if k is None else (q, k)
+    packed = q.dim() == 3
+    if not packed and q.dim() != 4:
+        raise ValueError("q must be [B, H, S, D], or packed [H, T, D]")
+    D = q.shape[-1]
+    tokens = q.shape[1:2] if packed else (q.shape[0], q.shape[2])
+    for x in xs:
+        if x.dtype != q.dtype or x.dim() != q.dim() or x.shape[-1] != D or \
+                (x.shape[1:2] if packed else (x.shape[0], x.shape[2])) != tokens:
+            raise ValueError(f"k {tuple(x.shape)} {x.dtype} does not match q {tuple(q.shape)} {q.dtype}")
+    dt, dev = _dt(q), _same_device(q, k, freqs, positions, cu_seqlens)
+    rot = _check_freqs(freqs, D)
+    B, S = (1, tokens[0]) if packed else tokens
+    pos, pos_stride, cu, nseq = None, 0, None, 0
+    if cu_seqlens is not None:
+        if not packed:
+            raise ValueError("cu_seqlens goes with packed [H, T, D] tensors")
+        cu, nseq = _int32(cu_seqlens, "cu_seqlens"), cu_seqlens.numel() - 1
+        if nseq < 0:
+            raise ValueError("cu_seqlens must hold at least one offset")
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != S or \
+                (positions.dim() == 2 and positions.shape[0] not in (1, B)) or \
+                (S > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be a CUDA int32 tensor of shape [{S}] or [{B}, {S}]")
+        pos = positions.data_ptr()
+        pos_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
+    elif packed and cu is None:
+        raise ValueError("packed tensors need cu_seqlens or positions")
+
+    def call(raw):
+        ys = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs) if out is None else \
+            (out,) if isinstance(out, torch.Tensor) else tuple(y for y in out if y is not None)
+        if len(ys) != len(xs):
+            raise ValueError("out must give a tensor for each input")
+        dims = (1, 0) if packed else (0, 1, 2)
+        rows = [], []
+        for i, (x, y) in enumerate(zip(xs, ys)):
+            if out is not None:
+                _check_rows_out(x, y, "out")
+            if i and ys[0].numel() and y.data_ptr() == ys[0].data_ptr():
+                raise ValueError("the two outputs are the same memory")
+            heads = x.shape[0] if packed else x.shape[1]
+            for t, to, is_out in ((x, rows[0], False), (y, rows[1], True)):
+                b, h, s = _strides(t, (0, 1, 2), is_out) if not packed else (0, *_strides(t, (0, 1), is_out))
+                to.append(_ROWS.pack(t.data_ptr(), b, h, s, heads))
+        if all(x.numel() == 0 for x in xs):
+            return (ys[0], None) if k is None else ys
+        st = fa_rope(b"".join(rows[0]), b"".join(rows[1]), len(xs), freqs.data_ptr(), rot, interleaved, float(amp),
+                     backward, pos, pos_stride, cu, nseq, B, S, D, dt, raw)
+        if st != FA_OK:
+            raise FAError(st, "fa_rope")
+        return (ys[0], None) if k is None else ys
+
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with _place(dev, stream) as raw:
+        return call(raw)
+
+
+def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved: bool = False, amp: float = 1.0, out=None,
+         stream=None):
+    """q and k (or None) with rotary positions, in one launch: [B, H, S, D]
+    tensors, or packed [H, T, D] ones with ``cu_seqlens``.  Inputs may be any
+    views whose rows are contiguous (a transposed projection, say); the
+    outputs are contiguous, or ``out`` = (q_out, k_out), which may be the
+    inputs themselves.  ``freqs`` and ``amp`` come from ``rope_freqs``;
+    ``positions`` (int32 [S] or [B, S]; packed [T]) defaults to the index in
+    the sequence.  The columns past the rotated ones are copied."""
+    return _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, False)
+
+
+def rope_backward(dq, dk, freqs, positions=None, cu_seqlens=None, interleaved: bool = False, amp: float = 1.0,
+                  out=None, stream=None):
+    """The gradients of ``rope``'s q and k from those of its outputs (as
+    ``backward`` / ``backward_varlen`` return them); arguments as ``rope``."""
+    return _rope(dq, dk, freqs, positions, cu_seqlens, interleaved, amp, out, stream, True)
+
+
+def _pages(k_pages, v_pages, block_table, B, dtype, D):
+    """The bytes of the fa_pages of these tensors, and the number of KV heads."""
+    import torch
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != dtype or v_pages.dtype != dtype:
+        raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D] of the queries' dtype")
+    n, heads, page, Dk = k_pages.shape
+    if Dk != D:
+        raise ValueError(f"pages of D = {Dk} do not match D = {D}")
+    inner, strides = (page * D, D, 1), []
+    for x in (k_pages, v_pages):
+        st = x.stride()
+        if st[1:] != inner and not (n and x[0].is_contiguous()):
+            raise ValueError("each page must be contiguous")
+        strides.append(st[0] if n > 1 else heads * page * D)
+    if strides[0] != strides[1]:
+        raise ValueError("k_pages and v_pages must have the same stride from page to page")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be a CUDA int32 tensor of shape [{B}, max_pages]")
+    row = block_table.stride(0) if B > 1 else 0
+    return _PAGES.pack(k_pages.data_ptr(), v_pages.data_ptr(), strides[0], block_table.data_ptr(), row, n, page, heads,
+                       block_table.shape[1]), heads
+
+
+def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, q=None, freqs=None, positions=None,
+                 interleaved: bool = False, amp: float = 1.0, q_out=None, stream=None):
+    """Write new keys and values into the pages of their sequences, the keys
+    (and the queries ``q`` of the same tokens) rotated on the way.
+
+    A decode step gives k, v [B, Hkv, D] (q [B, Hq, D]), one token per
+    sequence; with ``cu_seqlens`` they are packed [H, T, D].  ``seq_lens``
+    (CUDA int32 [B]) are the lengths with the new tokens, as ``decode_paged``
+    takes them next.  Without ``freqs`` nothing is rotated.  Returns the
+    rotated q (``q_out``, which may be q) or None.  Tokens of a sequence of
+    length 0 and tokens behind the last sequence write nothing; a row past
+    the table or a page outside the pool is reported by
+    ``check_device_error``."""
+    import torch
+    dev = _same_device(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
+    dt = _dt(k)
+    if k.dim() != 3 or k.shape != v.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be equal in shape and dtype: [B, Hkv, D], or packed [Hkv, T, D]")
+    one, D = cu_seqlens is None, k.shape[-1]
+    ht = (1, 0) if one else (0, 1)  # the dimensions of heads and tokens
+    T = k.shape[ht[1]]
+    B = T if one else cu_seqlens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must hold at least one offset")
+    pages, heads = _pages(k_pages, v_pages, block_table, B, k.dtype, D)
+    if k.shape[ht[0]] != heads:
+        raise ValueError(f"k has {k.shape[ht[0]]} heads, the pages {heads}")
+    lens = _int32(seq_lens, "seq_lens", (B,))
+    cu = None if one else _int32(cu_seqlens, "cu_seqlens")
+    pos = None if positions is None else _int32(positions, "positions", (T,))
+    rot = 0 if freqs is None else _check_freqs(freqs, D)
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
+    if q is not None:
+        if freqs is None:
+            raise ValueError("q is only rotated: it takes freqs")
+        if q.dim() != 3 or q.dtype != k.dtype or q.shape[ht[1]] != T or q.shape[-1] != D:
+            raise ValueError(f"q {tuple(q.shape)} {q.dtype} does not match k {tuple(k.shape)} {k.dtype}")
+
+    def call(raw):
+        to = torch.empty(q.shape, dtype=q.dtype, device=dev) if q is not None and q_out is None else q_out
+        if q_out is not None:
+            _check_rows_out(q, q_out, "q_out")
+
+        def rows(x, out=False):
+            h, t = _strides(x, ht, out)
+            return _ROWS.pack(x.data_ptr(), 0, h, t, x.shape[ht[0]])
+
+        if T == 0 or B == 0:
+            return to
+        st = fa_append_paged(rows(k), rows(v), None if q is None else rows(q), None if q is None else rows(to, True),
+                             pages, lens, cu, B, T, None if freqs is None else freqs.data_ptr(), rot, interleaved,
+                             float(amp), pos, D, dt, raw)
+        if st != FA_OK:
+            raise FAError(st, "fa_append_paged")
+        return to
+
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with _place(dev, stream) as raw:
+        return call(raw)
+
+
+def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, out, lse, workspace,
+                  stream):
+    import torch
+    dev = _same_device(q, k_pages, v_pages, block_table, seq_lens, prefix_table, out, lse, workspace)
+    dt = _dt(q)
+    if q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B, Hq, D] tensor")
+    B, Hq, D = q.shape
+    pages, heads = _pages(k_pages, v_pages, block_table, B, q.dtype, D)
+    lens = _int32(seq_lens, "seq_lens", (B,))
+    table = None
+    if prefix_table is not None:
+        table = _int32(prefix_table, "prefix_table")
+        if prefix_table.dim() != 1 or prefix_table.shape[0] * k_pages.shape[2] < prefix_len:
+            raise ValueError(f"prefix_table must name the pages of {prefix_len} rows")
+    if out is not None:
+        _check((out,), q.shape)
+        if out.dtype != q.dtype:
+            raise TypeError("out must have q's dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape [{B}, {Hq}]")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+
+    def call(raw):
+        o = torch.empty_like(q) if out is None else out
+        ll = torch.empty((B, Hq), device=dev, dtype=torch.float32) if lse is None else lse
+        ws = workspace
+        if ws is None:
+            need = fa_decode_prefix_workspace_size(B, Hq, heads, prefix_len, D)
+            ws = torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
+        size = ws.numel() * ws.element_size()
+        if prefix_len:
+            st = fa_decode_prefix(q.data_ptr(), pages, lens, prefix_len, table, o.data_ptr(), ll.data_ptr(), B, Hq, D,
+                                  scale, dt, ws.data_ptr(), size, raw)
+        else:
+            st = fa_decode_paged(q.data_ptr(), pages, lens, o.data_ptr(), ll.data_ptr(), B, Hq, D, scale, dt,
+                                 ws.data_ptr(), size, raw)
+        if st != FA_OK:
+            raise FAError(st, "fa_decode_prefix" if prefix_len else "fa_decode_paged")
+        return o, ll
+
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with _place(dev, stream) as raw:
+        return call(raw)
+
+
+def decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float | None = None, out=None, lse=None,
+                 workspace=None, stream=None):
+    """One decode step over a paged cache: q [B, Hq, D] against pages
+    [n_pages, Hkv, page_size, D] that ``block_table`` (CUDA int32
+    [B, max_pages]) names, ``seq_lens`` (CUDA int32 [B]) rows of each
+    sequence.  Returns O [B, Hq, D] and fp32 LSE [B, Hq]."""
+    return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, 0, None, scale, out, lse, workspace, stream)
+
+
+def decode_prefix(q, k_pages, v_pages, block_table, seq_lens, prefix_len: int, prefix_table=None,
+                  scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """``decode_paged`` for sequences whose first ``prefix_len`` rows (a
+    multiple of the page size) are the same pages: those named by
+    ``prefix_table``, or by the first row of ``block_table``.  The shared rows
+    are read once for the whole batch."""
+    return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, int(prefix_len), prefix_table, scale, out, lse,
+                         workspace, stream)
+
+
 def check_device_error(stream=None):
     """Synchronise and raise FAError if a kernel recorded an error (a wait
-    that timed out, or split backward calls that disagreed on the mode)."""
+    that timed out, split backward calls that disagreed on the mode, or a
+    page table that named a page outside its pool)."""
     st = fa_check_device_error(_stream(stream))
     if st != FA_OK:
         raise FAError(st, "device")

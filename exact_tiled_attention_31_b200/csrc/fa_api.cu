@@ -1,6 +1,7 @@
 // fa_api.cu - host side of the C ABI declared in include/fa.h: argument
 // checks, TMA tensor-map encoding, launch configuration and the device error
-// word.  All device work happens in the kernels of fa_fwd.cuh / fa_bwd.cuh.
+// word.  All device work happens in the kernels of fa_fwd.cuh / fa_bwd.cuh /
+// fa_decode.cuh; rotary positions and the paged cache are in fa_paged.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -17,26 +18,11 @@
 #include "fa_bwd.cuh"
 #include "fa_decode.cuh"
 #include "fa_fwd.cuh"
+#include "fa_host.cuh"
+
+std::atomic<uint64_t> fa_host::g_launches{0};
 
 namespace {
-
-std::atomic<uint64_t> g_launches{0};
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
 
 // [heads, rows, D] 16-bit tensor, boxes of box_rows rows x 64 columns, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, int D, long long rows, long long heads, bool bf16,
@@ -80,34 +66,6 @@ bool make_map_cols(CUtensorMap* m, const void* base, long long rows) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool scale_ok(float s) { return std::isfinite(s) && s > 0.f; }
-
-// Opt every kernel instance into its dynamic shared memory once per device
-// (one flag word per instance: the template argument is the kernel itself).
-template <auto Kernel>
-cudaError_t set_smem(uint32_t bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load() & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.fetch_or(bit);
-  return e;
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
-fa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // ---------------------------------------------------------------- forward
 template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool DROPOUT = false>
@@ -171,8 +129,6 @@ fa_status run_fwd(const void* q, const void* k, const void* v, void* o, float* l
 struct WsLayout {
   size_t dq_acc, cols, sem, ticket, total;
 };
-
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // heads x rows token rows in memory; per-query rows (16 bf16 each) padded per
 // sequence to ceil(S / 128) * 128 rows (S = the longest sequence)
@@ -341,12 +297,6 @@ fa_status bwd_common_checks(int B, int H, int S, int D, fa_dtype dt, const void*
   size_t need = ws_layout((long long)B * H, 1, S, S, D).total;
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
   return FA_OK;
-}
-
-bool ptrs_ok(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p || !aligned16(p)) return false;
-  return true;
 }
 
 // ---------------------------------------------------------------- error-path self-test
@@ -829,9 +779,12 @@ fa_status fa_check_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   uint32_t code = 0;
   if (cudaMemcpyFromSymbol(&code, fa::g_dev_error, sizeof(code)) != cudaSuccess) return FA_ERR_CUDA;
-  if (code == 0) return FA_OK;
   const uint32_t zero = 0;
-  if (cudaMemcpyToSymbol(fa::g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
+  if (code != 0 && cudaMemcpyToSymbol(fa::g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
+  uint32_t paged = 0;
+  if (fa_host::take_paged_error(&paged) != cudaSuccess) return FA_ERR_CUDA;
+  if (code == 0) code = paged;
+  if (code == 0) return FA_OK;
   return code == fa::DEV_ERR_ARG ? FA_ERR_INVALID_ARG : FA_ERR_TIMEOUT;
 }
 

@@ -1,0 +1,403 @@
+// fa_paged.cu - host side of the rotary-position, paged-cache and
+// shared-prefix entry points of include/fa.h: argument checks, tensor maps,
+// launch configuration.  The kernels are in fa_rope.cuh, fa_paged.cuh and
+// fa_prefix.cuh.
+#include <algorithm>
+
+#include "fa_host.cuh"
+#include "fa_prefix.cuh"
+#include "fa_rope.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------- shared checks
+bool rows_ok(const fa_rows* r) {
+  return r && r->data && aligned16(r->data) && r->batch_stride >= 0 && r->head_stride >= 0 && r->row_stride >= 0 &&
+         !(r->batch_stride & 7) && !(r->head_stride & 7) && !(r->row_stride & 7) && r->heads > 0;
+}
+bool ints_ok(const int* p) { return !(reinterpret_cast<uintptr_t>(p) & 3u); }
+
+fa::RowsIn rows_in(const fa_rows& r) {
+  return {static_cast<const uint16_t*>(r.data), r.batch_stride, r.head_stride, r.row_stride};
+}
+fa::RowsOut rows_out(const fa_rows& r) {
+  return {static_cast<uint16_t*>(r.data), r.batch_stride, r.head_stride, r.row_stride};
+}
+
+// Pages: a pool of n_pages x heads x page_size x D, 16-byte aligned; a table.
+fa_status pages_check(const fa_pages* pg, int D) {
+  if (!pg || pg->n_pages < 0 || pg->max_pages < 0 || pg->heads <= 0 || pg->page_size <= 0) return FA_ERR_INVALID_ARG;
+  if (pg->page_size < 16 || pg->page_size > 4096 || (pg->page_size & (pg->page_size - 1))) return FA_ERR_UNSUPPORTED;
+  if (!ptrs_ok({pg->k, pg->v}) || !pg->block_table || !ints_ok(pg->block_table)) return FA_ERR_INVALID_ARG;
+  if (pg->n_pages == 0 || pg->max_pages == 0) return FA_ERR_INVALID_ARG;
+  if ((pg->page_stride & 7) || pg->page_stride < (long long)pg->heads * pg->page_size * D) return FA_ERR_INVALID_ARG;
+  if (pg->table_stride < 0) return FA_ERR_INVALID_ARG;
+  if ((long long)pg->max_pages * pg->page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  // tensor-map limits: strides below 2^40 bytes
+  if (pg->page_stride >= (1LL << 39)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// ---------------------------------------------------------------- rotary positions
+// Heads a block walks over: all of them share a token's sines and cosines, but
+// below about eight blocks per SM a block takes fewer, down to one batch of
+// loads, so that few tokens still spread over the SMs.
+int heads_per_block(long long token_blocks, int heads) {
+  const long long want = 8LL * sm_count();
+  const long long groups = std::max(1LL, std::min<long long>((want + token_blocks - 1) / token_blocks,
+                                                             (heads + fa::kRopeBatch - 1) / fa::kRopeBatch));
+  const int per = (int)((heads + groups - 1) / groups);
+  return (per + fa::kRopeBatch - 1) / fa::kRopeBatch * fa::kRopeBatch;
+}
+
+template <int D, bool BF16>
+fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
+  constexpr int TOKENS = fa::kRopeThreads / (D / 16);
+  const long long blocks = ((long long)p.B * p.S + TOKENS - 1) / TOKENS;
+  const int heads = p.heads[0] + p.heads[1];
+  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  p.per = heads_per_block(blocks, heads);
+  const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
+  if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
+  if (inter) fa::rope_kernel<D, BF16, true><<<grid, fa::kRopeThreads, 0, st>>>(p);
+  else fa::rope_kernel<D, BF16, false><<<grid, fa::kRopeThreads, 0, st>>>(p);
+  g_launches.fetch_add(1);
+  return from_cuda(cudaGetLastError());
+}
+
+template <int D, bool BF16>
+fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
+  constexpr int TOKENS = fa::kRopeThreads / (D / 16);
+  const long long blocks = ((long long)p.T + TOKENS - 1) / TOKENS;
+  const int heads = p.Hq + 2 * p.Hkv;
+  p.per = heads_per_block(blocks, heads);
+  const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
+  if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
+  if (inter) fa::append_kernel<D, BF16, true><<<grid, fa::kRopeThreads, 0, st>>>(p);
+  else fa::append_kernel<D, BF16, false><<<grid, fa::kRopeThreads, 0, st>>>(p);
+  g_launches.fetch_add(1);
+  return from_cuda(cudaGetLastError());
+}
+
+bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0; }
+
+// ---------------------------------------------------------------- paged decode
+constexpr int kPagedGridMax = 1024;
+int paged_grid() { return std::min(sm_count(), kPagedGridMax); }
+
+// Ranges the shared rows are cut into: units = KV heads x query pairs CTAs run
+// one range each.  The cost of n ranges is waves x (tiles of the longest range
+// + the start and end of a CTA, about four tiles' worth); the fewest ranges of
+// the least cost are taken.
+int prefix_splits(long long units, int P) {
+  const long long tiles = ((long long)P + 127) / 128, sms = sm_count();
+  if (tiles <= 0) return 0;
+  long long best = 1, cost = -1;
+  for (long long n = 1; n <= std::min(64LL, tiles); ++n) {
+    const long long c = ((units * n + sms - 1) / sms) * ((tiles + n - 1) / n + 4);
+    if (cost < 0 || c < cost) best = n, cost = c;
+  }
+  return (int)best;
+}
+
+struct PagedWs {
+  size_t cuts, lse_part, o_part, pre_lse, pre_o, total;
+  int n_pre, n_pairs, per_tile;
+};
+
+PagedWs paged_layout(int B, int Hq, int Hkv, int P, int D) {
+  const int G = Hq / Hkv;
+  const size_t parts = (size_t)2 * paged_grid() * G;
+  PagedWs w;
+  w.per_tile = 128 / G;
+  w.n_pairs = (int)(((long long)B + 2 * w.per_tile - 1) / (2 * w.per_tile));
+  w.n_pre = P > 0 ? prefix_splits((long long)Hkv * w.n_pairs, P) : 0;
+  const size_t pre = (size_t)w.n_pre * B * Hq;
+  w.cuts = 0;
+  w.lse_part = up256(paged_grid() * sizeof(fa::PagedCut));
+  w.o_part = w.lse_part + up256(parts * 4);
+  w.pre_lse = w.o_part + up256(parts * D * 4);
+  w.pre_o = w.pre_lse + up256(pre * 4);
+  w.total = w.pre_o + up256(pre * D * 4);
+  return w;
+}
+
+// One K or V pool as (D, page_size, heads, pages), boxes of 64 columns x box rows.
+bool map_pages(CUtensorMap* m, const void* base, const fa_pages& pg, int D, bool bf16, int box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)pg.page_size, (cuuint64_t)pg.heads, (cuuint64_t)pg.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)pg.page_size * D * 2, (cuuint64_t)pg.page_stride * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+             dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q [B, Hkv, G, D] as (D, G, Hkv, B), boxes of 64 columns x G heads x per_tile sequences.
+bool map_queries(CUtensorMap* m, const void* q, int B, int Hkv, int G, int D, bool bf16, int per_tile) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)G * D * 2, (cuuint64_t)Hkv * G * D * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)per_tile}, estr[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(q), dims,
+             strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch that may begin before the kernel ahead of it on the stream ends;
+// the kernel itself waits (griddepcontrol.wait) before it reads what that wrote.
+template <typename... A>
+fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  return from_cuda(e);
+}
+
+template <int D, bool BF16, int NB>
+fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_t st) {
+  using C = fa::PagedCfg<D, NB>;
+  CUtensorMap mk, mv;
+  const int box = std::min(C::KT, pg.page_size);
+  if (!map_pages(&mk, pg.k, pg, D, BF16, box) || !map_pages(&mv, pg.v, pg, D, BF16, box)) return FA_ERR_CUDA;
+  if (set_smem<fa::paged_kernel<D, BF16, NB>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  fa::PagedParams a = p;
+  const long long tiles = std::max(1, (p.map.max_len - p.start + C::KT - 1) / C::KT);  // of the longest sequence
+  a.grid = (int)std::min<long long>(paged_grid(), (long long)p.B * p.Hkv * tiles);
+  if (p.n_pre) {
+    const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
+    if (s != FA_OK) return s;
+  } else {
+    fa::paged_kernel<D, BF16, NB><<<a.grid, C::THREADS, C::SMEM, st>>>(mk, mv, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return from_cuda(e);
+    g_launches.fetch_add(1);
+  }
+  if (tiles == 1) return FA_OK;  // a unit of one tile is never cut
+  return launch_after(fa::paged_merge_kernel<D, BF16>, dim3(a.grid, p.G), 128, 0, st, a);
+}
+
+template <int D, bool BF16>
+fa_status launch_prefix(const fa::PrefixParams& p, const void* q, const fa_pages& pg, cudaStream_t st) {
+  using C = fa::FwdCfg<D>;
+  CUtensorMap mq, mk, mv;
+  const int box = std::min(128, pg.page_size);
+  if (!map_queries(&mq, q, p.B, p.Hkv, p.G, D, BF16, p.per_tile) || !map_pages(&mk, pg.k, pg, D, BF16, box) ||
+      !map_pages(&mv, pg.v, pg, D, BF16, box))
+    return FA_ERR_CUDA;
+  if (set_smem<fa::prefix_kernel<D, BF16>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  const long long grid = (long long)p.n_pre * p.n_pairs * p.Hkv;
+  if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  fa::prefix_kernel<D, BF16><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  return from_cuda(e);
+}
+
+template <int D, bool BF16>
+fa_status run_paged(const fa::PagedParams& p, const fa::PrefixParams& pre, const void* q, const fa_pages& pg,
+                    cudaStream_t st) {
+  if (p.n_pre) {
+    const fa_status s = launch_prefix<D, BF16>(pre, q, pg, st);
+    if (s != FA_OK) return s;
+  }
+  return p.G <= 8 ? launch_paged<D, BF16, 1>(p, pg, st) : launch_paged<D, BF16, 2>(p, pg, st);
+}
+
+fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, int prefix_len, const int* prefix_table,
+                     void* o, float* lse, int B, int Hq, int D, float scale, fa_dtype dt, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (B < 0 || Hq < 0 || prefix_len < 0) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Hq == 0) return FA_OK;
+  const fa_status s = pages_check(pages, D);
+  if (s != FA_OK) return s;
+  const int Hkv = pages->heads, max_len = pages->max_pages * pages->page_size;
+  if (Hq % Hkv) return FA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;
+  if (prefix_len % pages->page_size || prefix_len > max_len) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (!ptrs_ok({q, o, lse}) || !seq_lens || !ints_ok(seq_lens) || !ints_ok(prefix_table)) return FA_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_INVALID_ARG;
+  const PagedWs w = paged_layout(B, Hq, Hkv, prefix_len, D);
+  if (workspace_bytes < w.total) return FA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fa::PagedParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.seq_lens = seq_lens;
+  p.map = {pages->block_table, pages->table_stride, pages->n_pages, log2_of(pages->page_size), max_len};
+  p.o_part = reinterpret_cast<float*>(ws + w.o_part);
+  p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
+  p.cuts = reinterpret_cast<fa::PagedCut*>(ws + w.cuts);
+  p.o = o;
+  p.lse = lse;
+  p.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+  p.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+  p.n_pre = w.n_pre, p.start = prefix_len;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  fa::PrefixParams pre = {};
+  pre.seq_lens = seq_lens;
+  pre.map = p.map;
+  if (prefix_table) pre.map.table = prefix_table;  // else the first sequence's row
+  pre.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+  pre.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+  pre.P = prefix_len, pre.n_pre = w.n_pre, pre.n_pairs = w.n_pairs, pre.per_tile = w.per_tile;
+  pre.B = B, pre.Hq = Hq, pre.Hkv = Hkv, pre.G = p.G;
+  pre.scale_log2 = p.scale_log2;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D == 128)
+    return dt == FA_BF16 ? run_paged<128, true>(p, pre, q, *pages, st) : run_paged<128, false>(p, pre, q, *pages, st);
+  return dt == FA_BF16 ? run_paged<64, true>(p, pre, q, *pages, st) : run_paged<64, false>(p, pre, q, *pages, st);
+}
+
+}  // namespace
+
+cudaError_t fa_host::take_paged_error(uint32_t* code) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, fa::g_dev_error, sizeof(*code));
+  if (e != cudaSuccess || *code == 0) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(fa::g_dev_error, &zero, sizeof(zero));
+}
+
+extern "C" {
+
+fa_status fa_rope_freqs(int rot_dim, double base, fa_rope_scaling scaling, double factor, int original_len,
+                        double beta_fast, double beta_slow, double* freqs, float* amp) {
+  constexpr double kTau = 6.283185307179586476925;
+  if (rot_dim <= 0 || rot_dim % 2 || !freqs || !amp) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || base <= 1.0) return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_PLAIN && scaling != FA_ROPE_LINEAR && scaling != FA_ROPE_NTK && scaling != FA_ROPE_YARN)
+    return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0)) return FA_ERR_INVALID_ARG;
+  if (scaling == FA_ROPE_NTK) {
+    if (rot_dim == 2) return FA_ERR_INVALID_ARG;
+    base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  }
+  double lo = 0, hi = 0;
+  if (scaling == FA_ROPE_YARN) {
+    if (original_len <= 0 || !std::isfinite(beta_fast) || !std::isfinite(beta_slow) || beta_slow <= 0 ||
+        beta_fast < beta_slow)
+      return FA_ERR_INVALID_ARG;
+    // the pair that turns `beta` times over the trained length
+    auto pair_of = [&](double beta) { return rot_dim * std::log(original_len / (beta * kTau)) / (2 * std::log(base)); };
+    lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
+    hi = std::min(std::ceil(pair_of(beta_slow)), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == FA_ROPE_LINEAR) f /= factor;
+    if (scaling == FA_ROPE_YARN) {
+      const double keep = 1.0 - std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 1e-3)));
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    freqs[i] = f;
+  }
+  *amp = scaling == FA_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return FA_OK;
+}
+
+fa_status fa_rope(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
+                  float amp, int backward, const int* positions, long long positions_stride, const int* cu_seqlens,
+                  int nseq, int B, int S, int D, fa_dtype dt, void* stream) {
+  if (B < 0 || S < 0 || nseq < 0 || positions_stride < 0 || n < 1 || n > 2 || !x || !y) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
+  if (cu_seqlens && B > 1) return FA_ERR_INVALID_ARG;
+  if (B == 0 || S == 0 || (cu_seqlens && nseq == 0)) return FA_OK;
+  if (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 7u) || !ints_ok(positions) || !ints_ok(cu_seqlens))
+    return FA_ERR_INVALID_ARG;
+  fa::RopeParams p = {};
+  for (int i = 0; i < n; ++i) {
+    if (!rows_ok(&x[i]) || !rows_ok(&y[i]) || x[i].heads != y[i].heads) return FA_ERR_INVALID_ARG;
+    p.x[i] = rows_in(x[i]);
+    p.y[i] = rows_out(y[i]);
+    p.heads[i] = x[i].heads;
+  }
+  if ((long long)p.heads[0] + p.heads[1] > 65535) return FA_ERR_UNSUPPORTED;
+  p.freqs = freqs, p.positions = positions, p.pos_batch = positions_stride;
+  p.cu = cu_seqlens, p.nseq = nseq, p.B = B, p.S = S, p.R = rot_dim;
+  p.amp = amp, p.sign = backward ? -1.f : 1.f;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool in = interleaved != 0;
+  if (D == 128) return dt == FA_BF16 ? launch_rope<128, true>(p, in, st) : launch_rope<128, false>(p, in, st);
+  return dt == FA_BF16 ? launch_rope<64, true>(p, in, st) : launch_rope<64, false>(p, in, st);
+}
+
+fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
+                          const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
+                          const double* freqs, int rot_dim, int interleaved, float amp, const int* positions, int D,
+                          fa_dtype dt, void* stream) {
+  if (nseq < 0 || total < 0) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (freqs && !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && nseq != total) return FA_ERR_INVALID_ARG;
+  if (nseq == 0 || total == 0) return FA_OK;
+  const fa_status s = pages_check(pages, D);
+  if (s != FA_OK) return s;
+  if (!rows_ok(k) || !rows_ok(v) || k->heads != pages->heads || v->heads != pages->heads) return FA_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q) || !rows_ok(q_out) || q->heads != q_out->heads || !freqs)) return FA_ERR_INVALID_ARG;
+  if (!seq_lens || !ints_ok(seq_lens) || !ints_ok(cu_seqlens) || !ints_ok(positions) ||
+      (reinterpret_cast<uintptr_t>(freqs) & 7u))
+    return FA_ERR_INVALID_ARG;
+  fa::AppendParams p = {};
+  p.k = rows_in(*k), p.v = rows_in(*v);
+  if (q) p.q = rows_in(*q), p.q_out = rows_out(*q_out), p.Hq = q->heads;
+  if ((long long)p.Hq + 2LL * pages->heads > 65535) return FA_ERR_UNSUPPORTED;
+  p.k_pages = static_cast<uint16_t*>(pages->k);
+  p.v_pages = static_cast<uint16_t*>(pages->v);
+  p.page_stride = pages->page_stride, p.table = pages->block_table, p.table_stride = pages->table_stride;
+  p.n_pages = pages->n_pages, p.page_shift = log2_of(pages->page_size), p.max_pages = pages->max_pages;
+  p.seq_lens = seq_lens, p.cu = cu_seqlens, p.freqs = freqs, p.positions = positions;
+  p.nseq = nseq, p.T = total, p.Hkv = pages->heads, p.R = freqs ? rot_dim : 0, p.amp = amp;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool in = interleaved != 0;
+  if (D == 128) return dt == FA_BF16 ? launch_append<128, true>(p, in, st) : launch_append<128, false>(p, in, st);
+  return dt == FA_BF16 ? launch_append<64, true>(p, in, st) : launch_append<64, false>(p, in, st);
+}
+
+size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int D) {
+  return fa_decode_prefix_workspace_size(B, Hq, Hkv, 0, D);
+}
+
+size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int D) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 16 || prefix_len < 0 || (D != 64 && D != 128)) return 0;
+  if ((long long)B * Hq > 0x7fffffffLL) return 0;
+  return paged_layout(B, Hq, Hkv, prefix_len, D).total;
+}
+
+fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_lens, void* o, float* lse, int B, int Hq,
+                          int D, float scale, fa_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_call(q, pages, seq_lens, 0, nullptr, o, lse, B, Hq, D, scale, dt, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_decode_prefix(const void* q, const fa_pages* pages, const int* seq_lens, int prefix_len,
+                           const int* prefix_table, void* o, float* lse, int B, int Hq, int D, float scale, fa_dtype dt,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_call(q, pages, seq_lens, prefix_len, prefix_table, o, lse, B, Hq, D, scale, dt, workspace,
+                    workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,575 @@
+// fa_paged.cuh - one decode step of exact attention over a paged KV cache.
+//
+// As in fa_decode.cuh each sequence brings one query token per query head,
+// query head h reads KV head h / G, and every row of the sequence is visible;
+// but the rows of sequence b live in pages: row i is row i % page_size of
+// page table[b][i / page_size] of a pool [n_pages, Hkv, page_size, D].
+//
+//   m = max_j s_j,  l = sum_j exp(s_j - m),  O = sum_j exp(s_j - m) v_j / l,
+// over the rows j in [start, len_b), one 64-row tile at a time; parts of a
+// sequence computed apart are joined by LSE = log sum exp(LSE_s),
+// O = sum exp(LSE_s - LSE) O_s.
+//
+// Bound: HBM, 4 D bytes a row and KV head, read once.  So the work is dealt
+// out by rows: the tiles of all (sequence, KV head) units, in order, are cut
+// into equal contiguous runs, one per SM, from the lengths on the device: a
+// ragged batch keeps every SM streaming to the end, whatever its lengths.
+// A unit that one run covers whole is finished there; the units cut by a
+// boundary (at most one per CTA) leave normalised fp32 parts that
+// paged_merge_kernel joins.
+//
+// Inside a CTA one producer warp fills a ring of stages (a tile's K and V
+// rows) by TMA, a box per page, and runs ahead of the consumers over unit
+// boundaries, so the stream does not pause when a unit ends.  Eight consumer
+// warps in two groups take alternate tiles, a warp 16 rows of each.  The
+// products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with the
+// cache rows (then the head's columns) as the 16-row side of m16n8k16: a
+// group of up to 8 query heads then pads to 8 instead of 16, and one ldmatrix
+// feeds a whole operand.
+#pragma once
+
+#include "fa_decode.cuh"
+
+namespace fa {
+
+struct PagedMap {       // how rows of a sequence are found
+  const int* table;     // [B, max_pages] by table_stride
+  long long table_stride;
+  int n_pages, page_shift, max_len;  // max_len: rows the table holds
+};
+
+// What CTA c left behind: the unit it began and did not finish, or bh = -1.
+struct PagedCut {
+  int b, kvh, last;  // the unit and the CTA that ends it; b = -1: none
+  int pad;
+};
+
+struct PagedParams {
+  const uint16_t* q;     // [B, Hq, D]
+  const int* seq_lens;   // [B]
+  PagedMap map;
+  float* o_part;         // [2 * grid, G, D] normalised parts: 2c for the unit CTA c goes on with, 2c + 1 begins
+  float* lse_part;       // [2 * grid, G] log2 of the sums
+  PagedCut* cuts;        // [grid]
+  void* o;               // [B, Hq, D]
+  float* lse;            // [B, Hq]
+  // parts over the shared rows [0, start) (start = 0: none)
+  const float* pre_o;    // [n_pre, B * Hq, D]
+  const float* pre_lse;  // [n_pre, B * Hq]
+  int n_pre, start;
+  int B, Hq, Hkv, G, grid;
+  float scale_log2;
+};
+
+template <int D, int NB>
+struct PagedCfg {
+  static constexpr int KT = 64;                        // rows per tile
+  static constexpr int ROWS = 8 * NB;                  // query rows, padded
+  static constexpr int HALF = KT * 128;                // 64 rows x 64 columns, 128-byte swizzled
+  static constexpr int TILE = KT * D * 2;              // K or V
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STAGES = D == 64 ? 10 : NB == 1 ? 5 : 4;  // 128 to 160 KB in flight
+  static constexpr int WARPS = 8;
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int OSTR = D + 4;                   // fp32 row stride of the scratch: conflict-free
+  static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats per warp
+  static constexpr uint32_t SMEM = STAGES * STAGE + WARPS * SCRATCH * 4 + 1024;
+  static_assert(SMEM <= 226 * 1024, "shared memory per block");
+};
+
+enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t movm_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Page of box `first row` of sequence b, or n_pages (out of the pool: TMA
+// fills zeros) with an argument error where the table names none.
+__device__ __forceinline__ int page_of(const PagedMap& m, const int* row, int first) {
+  const int id = row[first >> m.page_shift];
+  if (id >= 0 && id < m.n_pages) return id;
+  record_error(DEV_ERR_ARG, PAGED_SITE_PAGE);
+  return m.n_pages;
+}
+
+// O and LSE of one row from `n` parts and the shared rows' parts: a lane
+// holds VEC columns of the row.
+template <int VEC>
+struct RowSum {
+  float m = -INFINITY, w = 0.f, o[VEC];
+  __device__ __forceinline__ RowSum() {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = 0.f;
+  }
+  // a normalised part of logarithm l2 (log2; -inf: of no rows)
+  __device__ __forceinline__ void add(float l2, const float (&x)[VEC]) {
+    if (l2 == -INFINITY) return;
+    const float mn = fmaxf(m, l2), a = ex2(m - mn), b = ex2(l2 - mn);
+    w = w * a + b;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = o[i] * a + b * x[i];
+    m = mn;
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float (&x)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[VEC]) {
+  if constexpr (VEC == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+}
+// the finished row: O in 16 bits, LSE in natural units
+template <int VEC, bool BF16>
+__device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int D, int lane, const RowSum<VEC>& r) {
+  const float inv = r.w > 0.f ? 1.f / r.w : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + VEC * lane);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) dst[i] = pack2<BF16>(r.o[2 * i] * inv, r.o[2 * i + 1] * inv);
+  if (lane == 0) p.lse[row] = r.w > 0.f ? (r.m + __log2f(r.w)) * 0.69314718055994531f : -INFINITY;
+}
+
+// A place in the list of tiles: (sequence, KV head) units in order, each of
+// its sequence's tiles.  A sequence without rows of its own still has one
+// (empty) tile, so that its outputs are written.
+struct PagedWalk {
+  int b, kvh, tile, tiles, end;  // end: the sequence's length
+  __device__ __forceinline__ void load(const PagedParams& p, int KT) {
+    end = b < p.B ? min(max(p.seq_lens[b], 0), p.map.max_len) : 0;
+    tiles = max(1, (end - p.start + KT - 1) / KT);
+  }
+  __device__ __forceinline__ void next_unit(const PagedParams& p, int KT) {
+    tile = 0;
+    if (++kvh == p.Hkv) {
+      kvh = 0;
+      ++b;
+      load(p, KT);
+    }
+  }
+};
+
+template <int D, bool BF16, int NB>
+__global__ void __launch_bounds__(288, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const PagedParams p) {
+  using C = PagedCfg<D, NB>;
+  constexpr int VEC = D / 32;
+  extern __shared__ uint8_t dsm_raw[];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ long long warp_sum[C::WARPS], s_first;  // tiles before the first sequence of this run
+  __shared__ int s_b;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
+  float* scratch = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    s_b = 0;
+    s_first = 0;
+  }
+  pdl_launch();
+
+  // ---- this CTA's run [t0, t1) of the Hkv * sum_b tiles(b) tiles
+  auto tiles_of = [&](int b) {
+    const int end = min(max(p.seq_lens[b], 0), p.map.max_len);
+    return max(1, (end - p.start + C::KT - 1) / C::KT);
+  };
+  const int chunk = (p.B + 255) / 256;
+  const int b_lo = min((int)threadIdx.x * chunk, p.B), b_hi = threadIdx.x < 256 ? min(b_lo + chunk, p.B) : b_lo;
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (warp < C::WARPS && lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < C::WARPS; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  total *= p.Hkv;
+  const long long t0 = c * total / p.grid, t1 = (c + 1) * total / p.grid;
+  if (threadIdx.x < 256 && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
+    int b = b_lo;
+    for (; b < b_hi - 1; ++b) {
+      const int n = tiles_of(b);
+      if (t0 < (before + n) * p.Hkv) break;
+      before += n;
+    }
+    s_b = b;
+    s_first = before * p.Hkv;
+  }
+  __syncthreads();
+  PagedWalk at;
+  at.b = s_b;
+  at.load(p, C::KT);
+  at.kvh = (int)((t0 - s_first) / at.tiles);
+  at.tile = (int)((t0 - s_first) % at.tiles);
+  long long left = t1 - t0;
+
+  if (warp == C::WARPS) {
+    // ---------------------------------------------------------------- producer
+    const int box = min(C::KT, 1 << p.map.page_shift), boxes = C::KT / box;  // rows per box, boxes per tile
+    const int batch = 32 / boxes;                                            // tiles whose pages one load finds
+    const int copies = boxes * 2 * (D / 64);                                 // <= 16: one lane each
+    const int my_box = lane / (2 * (D / 64)), my_v = (lane / (D / 64)) & 1, my_half = lane % (D / 64);
+    uint32_t it = 0;
+    bool ok = true;
+    while (left > 0 && ok) {
+      const int n = (int)min((long long)(at.tiles - at.tile), left);
+      const int* row = p.map.table + at.b * p.map.table_stride;
+      // page of this lane's (tile, box) of the batch from tile k on
+      auto find = [&](int k) {
+        const int i = k + lane / boxes;
+        const int first = p.start + (at.tile + i) * C::KT + (lane % boxes) * box;
+        return i < n && lane < batch * boxes && first < at.end ? page_of(p.map, row, first) : -1;
+      };
+      int ids = find(0);
+      for (int k = 0; k < n && ok; k += batch) {
+        const int ids_next = find(k + batch);
+        for (int i = k; i < min(k + batch, n); ++i, ++it) {
+          const uint32_t st = it % C::STAGES, round = it / C::STAGES;
+          if (round > 0 &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (round - 1) & 1, PAGED_SITE_EMPTY))))
+            break;
+          const int key0 = p.start + (at.tile + i) * C::KT;
+          // boxes that hold rows of the sequence; the rest of the stage is left as it is and masked
+          const int live = at.end > key0 ? min(boxes, (at.end - key0 + box - 1) / box) : 0;
+          if (lane == 0) {
+            if (live) mbar_expect_tx(&full[st], live * box * D * 4);
+            else mbar_arrive(&full[st]);
+          }
+          __syncwarp();
+          const int id = __shfl_sync(0xffffffffu, ids, (i - k) * boxes + min(my_box, boxes - 1));
+          if (lane < copies && my_box < live) {
+            uint8_t* dst = ring + st * C::STAGE + my_v * C::TILE + my_half * C::HALF + my_box * box * 128;
+            const int first = key0 + my_box * box;
+            tma_load_4d(dst, my_v ? &tm_v : &tm_k, &full[st], 64 * my_half, first & ((1 << p.map.page_shift) - 1),
+                        at.kvh, id);
+          }
+        }
+        ids = ids_next;
+      }
+      left -= n;
+      if (left > 0) at.next_unit(p, C::KT);
+    }
+    // no copy may still be on its way into shared memory when the CTA ends
+    for (uint32_t f = it > C::STAGES ? it - C::STAGES : 0; f < it; ++f)
+      mbar_wait(&full[f % C::STAGES], (f / C::STAGES) & 1, PAGED_SITE_DRAIN);
+    __syncwarp();
+    pdl_wait();
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int grp = warp >> 2, wq = warp & 3;
+  const int r0 = 2 * (lane & 3);  // this lane's query rows 8 nb + r0, + 1; its cache rows lane / 4, + 8
+  float* ws = scratch + warp * C::SCRATCH;  // m[ROWS] l[ROWS] lr[ROWS] O[ROWS][OSTR]
+  uint32_t it = 0;
+  bool ok = true, waited = false;
+  PagedCut cut{-1, 0, 0, 0};
+  while (left > 0) {
+    const int n = (int)min((long long)(at.tiles - at.tile), left);
+    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
+    // Q^T as the B operand: column lane / 4 of each 8 is a query row
+    uint32_t qb[NB][D / 16][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + (lane >> 2);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (q_row + r) * D) + (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qb[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
+        qb[nb][kk][1] = r < p.G ? q[8 * kk + 4] : 0u;
+      }
+    }
+    float oacc[D / 16][NB][4];
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) oacc[mt][nb][0] = oacc[mt][nb][1] = oacc[mt][nb][2] = oacc[mt][nb][3] = 0.f;
+    float m[NB][2], l[NB][2], lr[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nb][e] = -INFINITY, l[nb][e] = lr[nb][e] = 0.f;
+
+    for (int i = 0; i < n; ++i, ++it) {
+      if ((int)(it & 1) != grp) continue;
+      const uint32_t st = it % C::STAGES;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / C::STAGES) & 1, PAGED_SITE_FULL));
+      if (!ok) continue;  // error recorded: take no more tiles, but keep to the barriers below
+      const int key0 = p.start + (at.tile + i) * C::KT + 16 * wq;  // this warp's 16 rows
+      const int live = at.end - key0;                              // how many of them are rows of the sequence
+      if (live > 0) {
+        const uint32_t ks = smem_addr(ring + st * C::STAGE), vs = ks + C::TILE;
+        // S^T = K Q^T
+        float s[NB][4];
+        {
+          float s2[NB][4];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nb][e] = s2[nb][e] = 0.f;
+          const int row = 16 * wq + (lane & 15);
+          const uint32_t base = ks + row * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4];
+            const int c8 = 2 * kk + (lane >> 4);
+            ldsm_x4(base + (c8 >> 3) * C::HALF + (((c8 & 7) ^ (row & 7)) << 4), a);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(kk & 1 ? s2[nb] : s[nb], a, qb[nb][kk][0], qb[nb][kk][1]);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nb][e] += s2[nb][e];
+        }
+        const int ka = lane >> 2;  // this lane's rows of the 16: ka, ka + 8
+        uint32_t pb[NB][2];
+        float alpha[NB][2];
+        bool grew = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float pv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // rows past the end drop out whatever they hold
+            pv[e] = ka + 8 * (e >> 1) < live ? s[nb][e] * p.scale_log2 : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(pv[e], pv[e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m[nb][e], mx);
+            alpha[nb][e] = mn > m[nb][e] ? ex2(m[nb][e] - mn) : 1.f;
+            grew |= mn > m[nb][e];
+            m[nb][e] = mn;
+            const float neg = mn == -INFINITY ? 0.f : mn;
+            pv[e] = ex2(pv[e] - neg);
+            pv[e + 2] = ex2(pv[e + 2] - neg);
+            l[nb][e] = l[nb][e] * alpha[nb][e] + (pv[e] + pv[e + 2]);
+          }
+          const uint32_t p0 = pack2<BF16>(pv[0], pv[1]), p1 = pack2<BF16>(pv[2], pv[3]);
+          const float2 w0 = unpack2<BF16>(p0), w1 = unpack2<BF16>(p1);
+          lr[nb][0] = lr[nb][0] * alpha[nb][0] + (w0.x + w1.x);
+          lr[nb][1] = lr[nb][1] * alpha[nb][1] + (w0.y + w1.y);
+          pb[nb][0] = movm_trans(p0);  // P^T as the B operand: its 8 x 8 blocks, transposed
+          pb[nb][1] = movm_trans(p1);
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) oacc[mt][nb][e] *= alpha[nb][e & 1];
+        }
+        // O^T += V^T P^T.  In a tile that runs past the end the rows behind it
+        // may hold anything (0 * inf): they are cleared in the operand.
+        uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
+        if (live < 16) {
+          keep_lo = (r0 < live ? 0xffffu : 0u) | (r0 + 1 < live ? 0xffff0000u : 0u);
+          keep_hi = (r0 + 8 < live ? 0xffffu : 0u) | (r0 + 9 < live ? 0xffff0000u : 0u);
+        }
+        const int row = 16 * wq + (lane & 7) + 8 * (lane >> 4);
+        const uint32_t base = vs + row * 128;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          uint32_t a[4];
+          const int c8 = 2 * mt + ((lane >> 3) & 1);
+          ldsm_x4_trans(base + (c8 >> 3) * C::HALF + (((c8 & 7) ^ (row & 7)) << 4), a);
+          a[0] &= keep_lo;
+          a[1] &= keep_lo;
+          a[2] &= keep_hi;
+          a[3] &= keep_hi;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(oacc[mt][nb], a, pb[nb][0], pb[nb][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    // ---- the eight warps' parts of the unit, through shared memory
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
+          lr[nb][e] += __shfl_xor_sync(0xffffffffu, lr[nb][e], o);
+        }
+        const int r = 8 * nb + r0 + e;
+        if (lane < 4) {
+          ws[r] = m[nb][e];
+          ws[C::ROWS + r] = l[nb][e];
+          ws[2 * C::ROWS + r] = lr[nb][e];
+        }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          float* dst = ws + 3 * C::ROWS + r * C::OSTR + 16 * mt + (lane >> 2);
+          dst[0] = oacc[mt][nb][e];
+          dst[8] = oacc[mt][nb][e + 2];
+        }
+      }
+    named_sync(1, 256);
+    if (p.n_pre && !waited) {  // the shared rows' parts come from the kernel before
+      pdl_wait();
+      waited = true;
+    }
+    const bool begins = at.tile == 0, ends = at.tile + n == at.tiles;
+    for (int r = warp; r < p.G; r += C::WARPS) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, scratch[w * C::SCRATCH + r]);
+      float lt = 0.f, lrt = 0.f, acc[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
+      if (mm != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float* x = scratch + w * C::SCRATCH;
+          const float f = ex2(x[r] - mm);
+          lt += f * x[C::ROWS + r];
+          lrt += f * x[2 * C::ROWS + r];
+          float ov[VEC];
+          load_vec<VEC>(x + 3 * C::ROWS + r * C::OSTR + VEC * lane, ov);
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) acc[v] += f * ov[v];
+        }
+      }
+      // O is normalised by the sum of the weights as rounded for the product,
+      // the logarithm is that of the fp32 sum
+      const float inv = lrt > 0.f ? 1.f / lrt : 0.f;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[v] *= inv;
+      const float l2 = lt > 0.f ? mm + __log2f(lt) : -INFINITY;
+      if (begins && ends) {
+        RowSum<VEC> sum;
+        sum.add(l2, acc);
+        const size_t row = q_row + r;
+        for (int s = 0; s < p.n_pre; ++s) {
+          const size_t pr = (size_t)s * p.B * p.Hq + row;
+          float x[VEC];
+          load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x);
+          sum.add(p.pre_lse[pr], x);
+        }
+        store_row<VEC, BF16>(p, row, D, lane, sum);
+      } else {
+        const size_t slot = (size_t)(2 * c + (begins ? 1 : 0)) * p.G + r;
+        store_vec<VEC>(p.o_part + slot * D + VEC * lane, acc);
+        if (lane == 0) p.lse_part[slot] = l2;
+      }
+    }
+    if (begins && !ends) {
+      // the CTA that runs the unit's last tile x: the largest c' with
+      // floor(c' total / grid) <= x
+      const long long x = t1 + (at.tiles - at.tile - n) - 1;
+      cut = PagedCut{at.b, at.kvh, (int)(((x + 1) * p.grid - 1) / total), 0};
+    }
+    named_sync(1, 256);  // the scratch is read before the next unit writes it
+    left -= n;
+    at.tile += n;
+    if (left > 0) at.next_unit(p, C::KT);
+  }
+  if (threadIdx.x == 0) p.cuts[c] = cut;
+  if (!waited) pdl_wait();
+}
+
+// The units that a boundary between CTAs cut: block (c, r) joins the parts of
+// query row r of the unit that CTA c began and did not finish, if any, with
+// the shared rows' parts.  Four warps take the parts in turn.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
+  constexpr int VEC = D / 32;
+  __shared__ float s_m[4], s_w[4], s_o[4][D];
+  pdl_wait();
+  const PagedCut cut = p.cuts[blockIdx.x];
+  if (cut.b < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
+  const size_t row = (size_t)cut.b * p.Hq + cut.kvh * p.G + r;
+  const int c0 = blockIdx.x, own = cut.last - c0 + 1, n = own + p.n_pre;
+  RowSum<VEC> sum;
+#pragma unroll 4
+  for (int s = warp; s < n; s += 4) {
+    float l2, x[VEC];
+    if (s < own) {
+      const size_t slot = (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r;
+      l2 = p.lse_part[slot];
+      load_vec<VEC>(p.o_part + slot * D + VEC * lane, x);
+    } else {
+      const size_t pr = (size_t)(s - own) * p.B * p.Hq + row;
+      l2 = p.pre_lse[pr];
+      load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x);
+    }
+    sum.add(l2, x);
+  }
+  store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
+  if (lane == 0) s_m[warp] = sum.m, s_w[warp] = sum.w;
+  __syncthreads();
+  if (warp) return;
+  RowSum<VEC> all;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) all.m = fmaxf(all.m, s_m[w]);
+  if (all.m != -INFINITY) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = ex2(s_m[w] - all.m);
+      all.w += f * s_w[w];
+      float x[VEC];
+      load_vec<VEC>(&s_o[w][VEC * lane], x);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) all.o[v] += f * x[v];
+    }
+  }
+  store_row<VEC, BF16>(p, row, D, lane, all);
+}
+
+}  // namespace fa

@@ -1,0 +1,260 @@
+// fa_rope.cuh - rotary positions, on tensors and on the way into a paged cache.
+//
+// Pair i (i < R / 2) of the first R of a row's D columns is a point of the
+// plane, turned by the angle pos * f_i and scaled by amp:
+//     (a, b) -> amp * (a cos - b sin, b cos + a sin),
+// and the columns from R on are copied.  The pairs are columns (i, i + R/2)
+// ("half") or (2i, 2i + 1) ("interleaved").  The map is linear, so the
+// gradient takes the transposed matrix: the same with the angle negated.
+//
+// Angles.  pos * f_i reaches 10^6 radians and more, where fp32 has lost the
+// phase.  The turns pos * f_i / 2 pi are formed in fp64 and reduced to
+// [-1/2, 1/2] there (error below 2^-34 turns up to position 2^20, 2^-23 at
+// 2^31); only the reduced turns go to fp32, for sincospif.
+//
+// Bound: HBM.  Every row is read once and written once, 2 x 2 D bytes, with
+// three multiply-adds a pair.  A thread owns two 8-column chunks of one
+// token that hold whole pairs (columns c and c + R/2 of the rotated part;
+// likewise of the copied part), forms their eight sines and cosines once and
+// then walks over the token's heads, four heads' loads at a time in flight.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace fa {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;  // heads whose loads a thread keeps in flight
+
+// A strided stack of rows of D contiguous 16-bit values (strides in elements).
+struct RowsIn {
+  const uint16_t* p;
+  long long batch, head, row;
+};
+struct RowsOut {
+  uint16_t* p;
+  long long batch, head, row;
+};
+
+// The place of token t of a packed batch: its sequence s in [0, nseq) by the
+// offsets cu[0 .. nseq], or -1 behind the last sequence (or before the first).
+__device__ __forceinline__ int seq_of(const int* cu, int nseq, int t) {
+  if (t < cu[0] || t >= cu[nseq]) return -1;
+  int lo = 0, hi = nseq;  // the number of offsets cu[1 ..] that are <= t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
+  }
+  return lo < nseq ? lo : -1;
+}
+
+__device__ __forceinline__ void rope_angle(double freq, int pos, float amp, float& c, float& s) {
+  double turns = (double)pos * (freq * 0.15915494309189533577);
+  turns -= rint(turns);
+  float sn, cs;
+  sincospif(2.f * (float)turns, &sn, &cs);
+  c = cs * amp;
+  s = sn * amp;
+}
+
+// The two 8-column chunks of item `it` (of D / 16 items), whether they are
+// rotated, and for pair j of the thread's eight its frequency index.
+template <int D, bool INTER>
+struct RopeItem {
+  int lo, hi;   // first columns of the two chunks
+  bool turn;
+  int f_lo, f_hi;
+  __device__ __forceinline__ RopeItem(int it, int R) {
+    turn = it < R / 16;
+    const int base = turn ? 0 : R, width = turn ? R : D - R, i = turn ? it : it - R / 16;
+    lo = base + 8 * i;
+    hi = lo + width / 2;
+    // half: pair j is (lo + j, hi + j), frequency lo + j; interleaved: each
+    // chunk holds four pairs, frequencies from half its first column on
+    f_lo = INTER ? lo / 2 : lo;
+    f_hi = INTER ? hi / 2 : lo + 4;
+  }
+};
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* y = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (INTER) {
+      const float2 u = unpack2<BF16>(x[j]), v = unpack2<BF16>(y[j]);
+      x[j] = pack2<BF16>(u.x * c[j] - u.y * s[j], u.y * c[j] + u.x * s[j]);
+      y[j] = pack2<BF16>(v.x * c[4 + j] - v.y * s[4 + j], v.y * c[4 + j] + v.x * s[4 + j]);
+    } else {
+      const float2 u = unpack2<BF16>(x[j]), v = unpack2<BF16>(y[j]);
+      x[j] = pack2<BF16>(u.x * c[2 * j] - v.x * s[2 * j], u.y * c[2 * j + 1] - v.y * s[2 * j + 1]);
+      y[j] = pack2<BF16>(v.x * c[2 * j] + u.x * s[2 * j], v.y * c[2 * j + 1] + u.y * s[2 * j + 1]);
+    }
+  }
+}
+
+struct RopeParams {
+  RowsIn x[2];
+  RowsOut y[2];
+  int heads[2];
+  const double* freqs;     // [R / 2] radians per position
+  const int* positions;    // [B, S] by pos_batch, or null: the index in the sequence
+  long long pos_batch;
+  const int* cu;           // packed batch (B = 1, S rows): [nseq + 1] offsets, or null
+  int nseq, B, S, R, per;  // per: heads a block walks over
+  float amp;
+  float sign;              // -1 turns back
+};
+
+// grid: (token tiles, head groups); block: tokens x D / 16 items
+template <int D, bool BF16, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
+  const int it = threadIdx.x % ITEMS;
+  const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  if (n >= (long long)p.B * p.S) return;
+  const int b = (int)(n / p.S), t = (int)(n - (long long)b * p.S);
+  int pos = t;
+  if (p.cu) {
+    const int s = seq_of(p.cu, p.nseq, t);
+    if (s < 0) return;  // rows of no sequence stay as they were
+    pos = t - p.cu[s];
+  }
+  if (p.positions) pos = p.positions[b * p.pos_batch + t];
+  const RopeItem<D, INTER> item(it, p.R);
+  const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads[0] + p.heads[1]);
+  // head h of both tensors' heads in one row: h < heads[0] is the first's
+  auto in = [&](int h) {
+    const int w = h >= p.heads[0];
+    return p.x[w].p + b * p.x[w].batch + (long long)(h - (w ? p.heads[0] : 0)) * p.x[w].head + t * p.x[w].row;
+  };
+  auto out = [&](int h) {
+    const int w = h >= p.heads[0];
+    return p.y[w].p + b * p.y[w].batch + (long long)(h - (w ? p.heads[0] : 0)) * p.y[w].head + t * p.y[w].row;
+  };
+  uint4 lo[kRopeBatch], hi[kRopeBatch];
+  float c[8], s[8];
+  for (int h = h0; h < h1; h += kRopeBatch) {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k)
+      if (h + k < h1) {
+        const uint16_t* x = in(h + k);
+        lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
+        hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
+      }
+    if (h == h0 && item.turn) {  // while the first loads are on their way
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
+        s[j] *= p.sign;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k)
+      if (h + k < h1) {
+        if (item.turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+        uint16_t* y = out(h + k);
+        *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
+        *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// New keys and values into the pages of their sequences.
+//
+// Token t is the j-th of the n new tokens of its sequence b; it becomes row
+// i = seq_lens[b] - n + j of the sequence, which lives in row i % page_size
+// of page table[b][i / page_size].  Its key is rotated by i (or positions[t])
+// on the way, its value copied, and the query of the same token, if given,
+// rotated into q_out by the same launch.  Tokens with i < 0 (a padded batch
+// gives its padding rows length 0) and tokens of no sequence write nothing.
+// A row past the table or a page outside the pool writes nothing and records
+// an argument error.
+// ---------------------------------------------------------------------------
+enum : uint32_t { APPEND_SITE_PAGE = 0x400 };
+
+struct AppendParams {
+  RowsIn q, k, v;  // batch unused
+  RowsOut q_out;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  long long page_stride;   // elements from one page to the next
+  const int* table;        // [nseq, max_pages] by table_stride
+  long long table_stride;
+  const int* seq_lens;     // [nseq], the new tokens included
+  const int* cu;           // [nseq + 1], or null: token t is the new one of sequence t
+  const double* freqs;     // null (R = 0): no rotation
+  const int* positions;    // [T], or null
+  int n_pages, page_shift, max_pages;
+  int nseq, T, Hq, Hkv, R, per;
+  float amp;
+};
+
+template <int D, bool BF16, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams p) {
+  constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
+  const int it = threadIdx.x % ITEMS;
+  const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  if (n >= p.T) return;
+  const int t = (int)n;
+  int b = t, i;
+  if (p.cu) {
+    b = seq_of(p.cu, p.nseq, t);
+    if (b < 0) return;
+    i = p.seq_lens[b] - (p.cu[b + 1] - t);
+  } else {
+    i = p.seq_lens[b] - 1;
+  }
+  if (i < 0) return;
+  const int pos = p.positions ? p.positions[t] : i;
+  const int slot = i >> p.page_shift, row = i & ((1 << p.page_shift) - 1);
+  const int page = slot < p.max_pages ? p.table[b * p.table_stride + slot] : -1;
+  const bool placed = page >= 0 && page < p.n_pages;
+  if (!placed && it == 0 && blockIdx.y == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
+  const long long at = placed ? page * p.page_stride + (long long)row * D : 0;
+  const RopeItem<D, INTER> item(it, p.R);
+  // heads in one row: q's Hq, k's Hkv, v's Hkv
+  const int hk = p.Hq, hv = p.Hq + p.Hkv;
+  const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, hv + p.Hkv);
+  auto in = [&](int h) {
+    return h < hk   ? p.q.p + h * p.q.head + t * p.q.row
+           : h < hv ? p.k.p + (h - hk) * p.k.head + t * p.k.row
+                    : p.v.p + (h - hv) * p.v.head + t * p.v.row;
+  };
+  auto out = [&](int h) -> uint16_t* {
+    if (h < hk) return p.q_out.p + h * p.q_out.head + t * p.q_out.row;
+    if (!placed) return nullptr;
+    const long long off = at + ((long long)(h < hv ? h - hk : h - hv) << p.page_shift) * D;
+    return (h < hv ? p.k_pages : p.v_pages) + off;
+  };
+  uint4 lo[kRopeBatch], hi[kRopeBatch];
+  float c[8], s[8];
+  for (int h = h0; h < h1; h += kRopeBatch) {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k)
+      if (h + k < h1) {
+        const uint16_t* x = in(h + k);
+        lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
+        hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
+      }
+    if (h == h0 && item.turn && h < hv) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
+    }
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k)
+      if (h + k < h1) {
+        if (item.turn && h + k < hv) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+        uint16_t* y = out(h + k);
+        if (y) {
+          *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
+          *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
+        }
+      }
+  }
+}
+
+}  // namespace fa

@@ -18,9 +18,9 @@ namespace fa {
 // ---------------------------------------------------------------------------
 enum : uint32_t { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_ARG = 2 };
 
-// Defined here: each shared library is built from a single translation unit.
-__device__ uint32_t g_dev_error = 0;   // first error code (0 = none)
-__device__ uint32_t g_dev_where = 0;   // site id of the first error
+// One pair per translation unit; fa_check_device_error() looks at each.
+static __device__ uint32_t g_dev_error = 0;   // first error code (0 = none)
+static __device__ uint32_t g_dev_where = 0;   // site id of the first error
 
 // Upper bound on any single barrier wait.  Every wait in a healthy launch
 // lasts microseconds; this bound only turns a logic error into a clean exit.

@@ -332,6 +332,145 @@ fa_status fa_decode(const void* q, const void* k_cache, const void* v_cache, con
                     float* lse, int B, int Hq, int Hkv, int L_max, int D, float scale, fa_dtype dt,
                     int n_splits, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Rotary positions, a paged KV cache and decode over it.  The pages describe
+ * none of these; they are what a caller of the attention above needs around
+ * it: positions rotated into q and k before fa_fwd / fa_fwd_varlen (and the
+ * gradient rotated back after fa_bwd / fa_bwd_varlen), and a cache that grows
+ * page by page for fa_decode's step.
+ */
+
+/* A strided stack of rows of D contiguous 16-bit values: element
+ * (b, h, t, d) is data[b * batch_stride + h * head_stride + t * row_stride + d].
+ * Strides are in elements, >= 0 and multiples of 8; data is 16-byte aligned.
+ * Inputs are only read. */
+typedef struct {
+  void* data;
+  long long batch_stride, head_stride, row_stride;
+  int heads;
+} fa_rows;
+
+/* A paged KV cache of the sequences of a batch.
+ *   k, v        pools [n_pages, heads, page_size, D], 16-bit, 16-byte aligned;
+ *               page_stride elements (a multiple of 8, at least
+ *               heads * page_size * D) from one page to the next, so k and v
+ *               may be interleaved in one allocation
+ *   block_table DEVICE int32 [B, max_pages], rows table_stride elements apart:
+ *               row i of sequence b is row i % page_size of page
+ *               block_table[b][i / page_size].  Entries past a sequence's
+ *               length are never read.
+ *   page_size   a power of two, 16 to 4096 (FA_ERR_UNSUPPORTED otherwise)
+ * max_pages * page_size may be at most 2^30. */
+typedef struct {
+  void* k;
+  void* v;
+  long long page_stride;
+  const int* block_table;
+  long long table_stride;
+  int n_pages, page_size, heads, max_pages;
+} fa_pages;
+
+typedef enum { FA_ROPE_PLAIN = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_YARN = 3 } fa_rope_scaling;
+
+/*
+ * Rotary frequencies, computed on the HOST: freqs[i], i < rot_dim / 2, in
+ * radians per position, and the factor *amp that the rotated columns take.
+ *   PLAIN   base^(-2i / rot_dim)
+ *   LINEAR  the same / factor (position interpolation)
+ *   NTK     PLAIN with base * factor^(rot_dim / (rot_dim - 2))
+ *   YARN    (Peng et al. 2023) pairs that turn more than beta_fast times over
+ *           original_len positions keep PLAIN, those below beta_slow turns take
+ *           LINEAR, a linear ramp in i between; *amp = 0.1 ln(factor) + 1
+ * factor >= 1.  Other schemes need no support here: fa_rope takes any table.
+ */
+fa_status fa_rope_freqs(int rot_dim, double base, fa_rope_scaling scaling, double factor, int original_len,
+                        double beta_fast, double beta_slow, double* freqs, float* amp);
+
+/*
+ * Rotary positions on one or two tensors (n = 1 or 2: q, or q and k of the
+ * same tokens) in one launch.  With a_i = pos * freqs[i]:
+ *   (u, w) -> amp * (u cos a_i - w sin a_i, w cos a_i + u sin a_i)
+ * for the rot_dim / 2 pairs of the first rot_dim columns of every row, the
+ * other columns copied.  The pairs are columns (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) if interleaved != 0.  backward != 0 applies the transposed map
+ * (the angle negated): the gradient of x from that of y.
+ *   x, y    n inputs and outputs with equal `heads`; y[i] may be x[i] itself
+ *           (same data and strides), any other overlap of an output with an
+ *           input or output is not allowed
+ *   freqs   DEVICE double [rot_dim / 2]; angles are reduced in fp64, so
+ *           positions may be any int32
+ *   dense   (cu_seqlens = NULL): [B, heads, S] rows; the position of row t is
+ *           positions[b * positions_stride + t], or t if positions is NULL
+ *   packed  (cu_seqlens: DEVICE int32 [nseq + 1], B = 1, S = total rows): the
+ *           position counts from the row's own sequence, or is positions[t];
+ *           rows behind cu_seqlens[nseq] are left as they were
+ * rot_dim is a multiple of 16, 16 <= rot_dim <= D (FA_ERR_UNSUPPORTED
+ * otherwise).  B = 0 or S = 0 is a no-op.
+ */
+fa_status fa_rope(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
+                  float amp, int backward, const int* positions, long long positions_stride, const int* cu_seqlens,
+                  int nseq, int B, int S, int D, fa_dtype dt, void* stream);
+
+/*
+ * New keys and values into the pages of their sequences, keys rotated on the
+ * way, and the queries of the same tokens rotated by the same launch.
+ *   k, v      [heads, total] rows (batch_stride unused), heads = pages->heads
+ *   q, q_out  [Hq, total] rows, or both NULL; q_out may be q itself
+ *   seq_lens  DEVICE int32 [nseq]: each sequence's length with its new tokens
+ *   cu_seqlens DEVICE int32 [nseq + 1]: token t is a new one of the sequence s
+ *             with cu_seqlens[s] <= t < cu_seqlens[s + 1]; NULL: total = nseq
+ *             and token t is the one new token of sequence t (a decode step)
+ * The j-th of n new tokens of sequence s becomes row i = seq_lens[s] - n + j.
+ * Keys and queries are rotated by position i, or positions[t] if given (DEVICE
+ * int32 [total]), as fa_rope does; freqs = NULL appends without rotation (q
+ * must be NULL).  Tokens with i < 0 (padding: length 0) and tokens behind
+ * cu_seqlens[nseq] write nothing.  A row past the table, or a page outside
+ * [0, n_pages), is not written, and fa_check_device_error() then returns
+ * FA_ERR_INVALID_ARG.  Two tokens of one call must not fall on one row.
+ */
+fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
+                          const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
+                          const double* freqs, int rot_dim, int interleaved, float amp, const int* positions, int D,
+                          fa_dtype dt, void* stream);
+
+/*
+ * fa_decode over a paged cache: for b < B, h < Hq, G = Hq / pages->heads,
+ *   O[b,h,:] = softmax(q[b,h,:] . K_b[h/G,j,:] * scale, j < len_b) V_b[h/G,:,:]
+ * with K_b, V_b the rows of sequence b's pages and len_b = seq_lens[b] clamped
+ * to [0, max_pages * page_size]; lse[b,h] the log-sum-exp.  len_b = 0 gives
+ * O = 0 and lse = -inf.
+ *   q, o  [B, Hq, D] 16-bit, contiguous;  lse fp32 [B, Hq]
+ *   workspace  at least fa_decode_paged_workspace_size(B, Hq, Hkv, D) bytes of
+ *         device memory, 256-byte aligned; contents on entry do not matter
+ * Pages may hold anything (NaN too) in rows at or past len_b.  A page outside
+ * [0, n_pages) counts as zeros and fa_check_device_error() then returns
+ * FA_ERR_INVALID_ARG.  Hq a multiple of Hkv, G <= 16.  The work is cut by the
+ * lengths on the device, so one recorded graph serves all lengths.
+ */
+/* The two-phase size query ("ops-transformer里的完整算子"); the size is for the
+ * current device (one part per SM boundary).  0 for unsupported arguments. */
+size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int D);
+fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_lens, void* o, float* lse, int B, int Hq,
+                          int D, float scale, fa_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_decode_paged for sequences that share their first prefix_len rows: the
+ * same result, with the shared rows read once for the whole batch.
+ *   prefix_len    a multiple of page_size, 0 <= prefix_len <= max_pages *
+ *                 page_size (0: fa_decode_paged)
+ *   prefix_table  DEVICE int32 [prefix_len / page_size], the shared rows'
+ *                 pages; NULL: those of block_table's first row
+ * block_table and seq_lens are those of fa_decode_paged: rows from prefix_len
+ * on are found in each sequence's own row of the table, and a sequence shorter
+ * than prefix_len sees the first len_b shared rows.  Every shared row must
+ * hold finite values.
+ */
+/* The two-phase size query ("ops-transformer里的完整算子"), for the current device. */
+size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int D);
+fa_status fa_decode_prefix(const void* q, const fa_pages* pages, const int* seq_lens, int prefix_len,
+                           const int* prefix_table, void* o, float* lse, int B, int Hq, int D, float scale, fa_dtype dt,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* A static, human-readable name for a status code.  No page defines status
  * codes; they are this library's error reporting. */
 const char* fa_status_string(fa_status s);
@@ -340,7 +479,7 @@ const char* fa_status_string(fa_status s);
  * Synchronises `stream`, then reads and clears the calling device's error
  * word.  Returns FA_OK, FA_ERR_TIMEOUT (a kernel gave up waiting),
  * FA_ERR_INVALID_ARG (fa_bwd_finish was told another deterministic mode
- * than fa_bwd_main ran in) or FA_ERR_CUDA (the synchronisation itself
+ * than fa_bwd_main ran in, or a page table named a page outside its pool) or FA_ERR_CUDA (the synchronisation itself
  * failed).  No page defines this
  * call; it is the host side of the library's bounded-wait error handling.
  */
