@@ -232,7 +232,10 @@ __global__ void __launch_bounds__(288, 1)
     total += warp_sum[w];
   }
   total *= p.Hkv;
-  const long long t0 = c * total / p.grid, t1 = (c + 1) * total / p.grid;
+  // with fewer tiles than CTAs the last CTAs have none, so that no CTA inside a
+  // unit's range is without a part
+  const int runs = (int)min((long long)p.grid, total);
+  const long long t0 = c < runs ? c * total / runs : 0, t1 = c < runs ? (c + 1) * total / runs : 0;
   if (threadIdx.x < 256 && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
     int b = b_lo;
     for (; b < b_hi - 1; ++b) {
@@ -510,9 +513,9 @@ __global__ void __launch_bounds__(288, 1)
     }
     if (begins && !ends) {
       // the CTA that runs the unit's last tile x: the largest c' with
-      // floor(c' total / grid) <= x
+      // floor(c' total / runs) <= x
       const long long x = t1 + (at.tiles - at.tile - n) - 1;
-      cut = PagedCut{at.b, at.kvh, (int)(((x + 1) * p.grid - 1) / total), 0};
+      cut = PagedCut{at.b, at.kvh, (int)(((x + 1) * runs - 1) / total), 0};
     }
     named_sync(1, 256);  // the scratch is read before the next unit writes it
     left -= n;

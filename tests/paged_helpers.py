@@ -57,7 +57,7 @@ def check_decode(o, lse, q, ref, what):
     err, tol = np.abs(go - ro), u * np.abs(ro) + TINY + (2 * u + 2 * (2 * e_s[..., None] + 2.0 ** -21)) * mean_v
     bad = np.unravel_index((err - tol).argmax(), err.shape)
     assert (err <= tol).all(), f"{what}: O {go[bad]} vs {ro[bad]} (tolerance {tol[bad]:.3g}) at {bad}"
-    err = np.abs(gl - rl, where=~empty, out=np.zeros_like(gl))
+    err = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, rl))
     tol = 2 * e_s + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(empty, 0, rl))
     bad = np.unravel_index((err - tol).argmax(), err.shape)
     assert (err <= tol).all(), f"{what}: LSE {gl[bad]} vs {rl[bad]} (tolerance {tol[bad]:.3g}) at {bad}"
