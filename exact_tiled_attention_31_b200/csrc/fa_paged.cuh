@@ -68,13 +68,18 @@ struct PagedCfg {
   static constexpr int HALF = KT * 128;                // 64 rows x 64 columns, 128-byte swizzled
   static constexpr int TILE = KT * D * 2;              // K or V
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int STAGES = D == 64 ? 10 : NB == 1 ? 5 : 4;  // 128 to 160 KB in flight
+  // 128 to 192 KB in flight.  Even: tiles alternate between the two consumer
+  // groups, so a stage then belongs to one group, which sees every phase of its
+  // barrier.  (With an odd count a group would meet a stage every second phase,
+  // and a wait by parity cannot tell a phase from the one two before it.)
+  static constexpr int STAGES = D == 64 ? 10 : NB == 1 ? 6 : 4;
+  static_assert(STAGES % 2 == 0, "a stage belongs to one consumer group");
   static constexpr int WARPS = 8;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int OSTR = D + 4;                   // fp32 row stride of the scratch: conflict-free
   static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats per warp
   static constexpr uint32_t SMEM = STAGES * STAGE + WARPS * SCRATCH * 4 + 1024;
-  static_assert(SMEM <= 226 * 1024, "shared memory per block");
+  static_assert(SMEM + 256 <= 227 * 1024, "shared memory per block, the barriers and the run's place included");
 };
 
 enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
@@ -532,7 +537,8 @@ __global__ void __launch_bounds__(288, 1)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   constexpr int VEC = D / 32;
-  __shared__ float s_m[4], s_w[4], s_o[4][D];
+  __shared__ __align__(16) float s_o[4][D];
+  __shared__ float s_m[4], s_w[4];
   pdl_wait();
   const PagedCut cut = p.cuts[blockIdx.x];
   if (cut.b < 0) return;

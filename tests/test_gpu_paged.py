@@ -164,6 +164,17 @@ def test_decode_shapes(cuda_device, lens, Hq, Hkv, D, page):
     _decode_case(cuda_device, lens, Hq, Hkv, D, page, "bf16", seed=len(lens), pool2=True)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 4, 128, 64), (16, 1, 128, 16), (2, 2, 64, 128)])
+def test_decode_long_runs(cuda_device, Hq, Hkv, D, page):
+    """Every CTA's ring goes round several times, over the ends of units too, and call follows call."""
+    lens = [16384 // Hkv, 4100, 16384, 8000, 13001]
+    args, o, lse = _decode_case(cuda_device, [n * (4 // Hkv + 1) // 2 for n in lens], Hq, Hkv, D, page, "bf16", seed=D + page)
+    for _ in range(20):
+        again = fa.decode_paged(*args, scale=D ** -0.5)
+    fa.check_device_error()
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 def test_decode_large_scores(cuda_device):
     """Scores of hundreds: the exact maximum keeps every exponent at or below zero."""
     _decode_case(cuda_device, [2000, 77], 8, 2, 128, 64, "bf16", seed=4, mult=8.0)
