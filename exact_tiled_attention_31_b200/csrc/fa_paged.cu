@@ -33,8 +33,8 @@ fa_status pages_check(const fa_pages* pg, int D) {
   if ((pg->page_stride & 7) || pg->page_stride < (long long)pg->heads * pg->page_size * D) return FA_ERR_INVALID_ARG;
   if (pg->table_stride < 0) return FA_ERR_INVALID_ARG;
   if ((long long)pg->max_pages * pg->page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
-  // tensor-map limits: strides below 2^40 bytes
-  if (pg->page_stride >= (1LL << 39)) return FA_ERR_UNSUPPORTED;
+  // tensor-map limits: strides below 2^40 bytes, coordinates below 2^31
+  if (pg->page_stride >= (1LL << 39) || (long long)pg->heads * pg->page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -128,14 +128,16 @@ PagedWs paged_layout(int B, int Hq, int Hkv, int P, int D) {
   return w;
 }
 
-// One K or V pool as (D, page_size, heads, pages), boxes of 64 columns x box rows.
+// One K or V pool as (64 columns, 8 rows, D / 64 halves, 8-row groups of all
+// heads, pages), boxes of box whole rows (load_rows).
 bool map_pages(CUtensorMap* m, const void* base, const fa_pages& pg, int D, bool bf16, int box) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)pg.page_size, (cuuint64_t)pg.heads, (cuuint64_t)pg.n_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)pg.page_size * D * 2, (cuuint64_t)pg.page_stride * 2};
-  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+  const cuuint32_t halves = D / 64;
+  const cuuint64_t dims[5] = {64, 8, halves, (cuuint64_t)pg.heads * pg.page_size / 8, (cuuint64_t)pg.n_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16, (cuuint64_t)pg.page_stride * 2};
+  const cuuint32_t boxes[5] = {64, 8, halves, (cuuint32_t)box / 8, 1}, estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base),
              dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

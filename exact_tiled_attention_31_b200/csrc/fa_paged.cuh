@@ -65,7 +65,7 @@ template <int D, int NB>
 struct PagedCfg {
   static constexpr int KT = 64;                        // rows per tile
   static constexpr int ROWS = 8 * NB;                  // query rows, padded
-  static constexpr int HALF = KT * 128;                // 64 rows x 64 columns, 128-byte swizzled
+  static constexpr int GROUP = D * 16;                 // 8 rows: D / 64 swizzle atoms of 1 KB
   static constexpr int TILE = KT * D * 2;              // K or V
   static constexpr int STAGE = 2 * TILE;
   // 128 to 192 KB in flight.  Even: tiles alternate between the two consumer
@@ -90,6 +90,20 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uin
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+// Rows of one page and KV head into shared memory.  The pool is viewed as
+// (64 columns, 8 rows, D / 64 halves, 8-row groups of all heads, pages), so
+// that one copy brings whole rows and leaves them as [group][half][8][128
+// bytes]: 8-row groups D / 64 KB apart, whatever the page size, each half an
+// atom of the 128-byte swizzle.  (Boxes of 64 columns x rows need two copies
+// for D = 128; with 16-row pages the copies, at about 65 ns each an SM, then
+// bound decode at 4.1 to 4.6 TB/s.)
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* m, uint64_t* bar, int group, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(group), "r"(page), "r"(smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -164,6 +178,28 @@ __device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int 
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) dst[i] = pack2<BF16>(r.o[2 * i] * inv, r.o[2 * i + 1] * inv);
   if (lane == 0) p.lse[row] = r.w > 0.f ? (r.m + __log2f(r.w)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The shared rows' parts s = first, first + step, ... of a row, eight parts'
+// loads in flight (one part at a time took a memory latency each: 16 us a unit
+// with 16 parts).
+template <int VEC>
+__device__ __forceinline__ void add_shared(const PagedParams& p, size_t row, int D, int lane, int first, int step,
+                                           RowSum<VEC>& sum) {
+  constexpr int FLY = 8;
+  const size_t rows = (size_t)p.B * p.Hq;
+  for (int s = first; s < p.n_pre; s += FLY * step) {
+    float l2[FLY], x[FLY][VEC];
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) {
+      const size_t pr = (size_t)(s + k * step) * rows + row;
+      const bool in = s + k * step < p.n_pre;
+      l2[k] = in ? p.pre_lse[pr] : -INFINITY;
+      if (in) load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) sum.add(l2[k], x[k]);
+  }
 }
 
 // A place in the list of tiles: (sequence, KV head) units in order, each of
@@ -263,8 +299,7 @@ __global__ void __launch_bounds__(288, 1)
     // ---------------------------------------------------------------- producer
     const int box = min(C::KT, 1 << p.map.page_shift), boxes = C::KT / box;  // rows per box, boxes per tile
     const int batch = 32 / boxes;                                            // tiles whose pages one load finds
-    const int copies = boxes * 2 * (D / 64);                                 // <= 16: one lane each
-    const int my_box = lane / (2 * (D / 64)), my_v = (lane / (D / 64)) & 1, my_half = lane % (D / 64);
+    const int my_box = lane >> 1, my_v = lane & 1;                           // the copy this lane issues: <= 8 of them
     uint32_t it = 0;
     bool ok = true;
     while (left > 0 && ok) {
@@ -293,11 +328,10 @@ __global__ void __launch_bounds__(288, 1)
           }
           __syncwarp();
           const int id = __shfl_sync(0xffffffffu, ids, (i - k) * boxes + min(my_box, boxes - 1));
-          if (lane < copies && my_box < live) {
-            uint8_t* dst = ring + st * C::STAGE + my_v * C::TILE + my_half * C::HALF + my_box * box * 128;
-            const int first = key0 + my_box * box;
-            tma_load_4d(dst, my_v ? &tm_v : &tm_k, &full[st], 64 * my_half, first & ((1 << p.map.page_shift) - 1),
-                        at.kvh, id);
+          if (my_box < live) {
+            uint8_t* dst = ring + st * C::STAGE + my_v * C::TILE + my_box * box * D * 2;
+            const int first = (key0 + my_box * box) & ((1 << p.map.page_shift) - 1);  // row in its page
+            load_rows(dst, my_v ? &tm_v : &tm_k, &full[st], ((at.kvh << p.map.page_shift) + first) >> 3, id);
           }
         }
         ids = ids_next;
@@ -364,12 +398,12 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nb][e] = s2[nb][e] = 0.f;
           const int row = 16 * wq + (lane & 15);
-          const uint32_t base = ks + row * 128;
+          const uint32_t base = ks + (row >> 3) * C::GROUP + (row & 7) * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t a[4];
             const int c8 = 2 * kk + (lane >> 4);
-            ldsm_x4(base + (c8 >> 3) * C::HALF + (((c8 & 7) ^ (row & 7)) << 4), a);
+            ldsm_x4(base + (kk >> 2) * 1024 + (((c8 & 7) ^ (row & 7)) << 4), a);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(kk & 1 ? s2[nb] : s[nb], a, qb[nb][kk][0], qb[nb][kk][1]);
           }
@@ -426,12 +460,12 @@ __global__ void __launch_bounds__(288, 1)
           keep_hi = (r0 + 8 < live ? 0xffffu : 0u) | (r0 + 9 < live ? 0xffff0000u : 0u);
         }
         const int row = 16 * wq + (lane & 7) + 8 * (lane >> 4);
-        const uint32_t base = vs + row * 128;
+        const uint32_t base = vs + (row >> 3) * C::GROUP + (row & 7) * 128;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
           uint32_t a[4];
           const int c8 = 2 * mt + ((lane >> 3) & 1);
-          ldsm_x4_trans(base + (c8 >> 3) * C::HALF + (((c8 & 7) ^ (row & 7)) << 4), a);
+          ldsm_x4_trans(base + (mt >> 2) * 1024 + (((c8 & 7) ^ (row & 7)) << 4), a);
           a[0] &= keep_lo;
           a[1] &= keep_lo;
           a[2] &= keep_hi;
@@ -503,12 +537,7 @@ __global__ void __launch_bounds__(288, 1)
         RowSum<VEC> sum;
         sum.add(l2, acc);
         const size_t row = q_row + r;
-        for (int s = 0; s < p.n_pre; ++s) {
-          const size_t pr = (size_t)s * p.B * p.Hq + row;
-          float x[VEC];
-          load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x);
-          sum.add(p.pre_lse[pr], x);
-        }
+        add_shared<VEC>(p, row, D, lane, 0, 1, sum);
         store_row<VEC, BF16>(p, row, D, lane, sum);
       } else {
         const size_t slot = (size_t)(2 * c + (begins ? 1 : 0)) * p.G + r;
@@ -544,22 +573,16 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   if (cut.b < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
   const size_t row = (size_t)cut.b * p.Hq + cut.kvh * p.G + r;
-  const int c0 = blockIdx.x, own = cut.last - c0 + 1, n = own + p.n_pre;
+  const int c0 = blockIdx.x, own = cut.last - c0 + 1;
   RowSum<VEC> sum;
 #pragma unroll 4
-  for (int s = warp; s < n; s += 4) {
-    float l2, x[VEC];
-    if (s < own) {
-      const size_t slot = (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r;
-      l2 = p.lse_part[slot];
-      load_vec<VEC>(p.o_part + slot * D + VEC * lane, x);
-    } else {
-      const size_t pr = (size_t)(s - own) * p.B * p.Hq + row;
-      l2 = p.pre_lse[pr];
-      load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x);
-    }
-    sum.add(l2, x);
+  for (int s = warp; s < own; s += 4) {
+    const size_t slot = (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r;
+    float x[VEC];
+    load_vec<VEC>(p.o_part + slot * D + VEC * lane, x);
+    sum.add(p.lse_part[slot], x);
   }
+  add_shared<VEC>(p, row, D, lane, warp, 4, sum);
   store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
   if (lane == 0) s_m[warp] = sum.m, s_w[warp] = sum.w;
   __syncthreads();

@@ -120,9 +120,8 @@ __global__ void __launch_bounds__(768, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       const int box = min(128, 1 << p.map.page_shift), boxes = 128 / box;  // rows per box, boxes per tile: <= 8
-      const int my_box = (int)lane / C::CH, my_half = (int)lane % C::CH;
+      const int my_box = (int)lane;
       const bool active = my_box < boxes;
-      const uint32_t off = my_half * C::CHUNK + my_box * box * 128;
       // page of this lane's box of tile j; past the shared rows zeros are filled
       auto find = [&](int j) {
         const int first = (j0 + j) * 128 + my_box * box;
@@ -150,9 +149,9 @@ __global__ void __launch_bounds__(768, 1)
         if (lane == 0) mbar_expect_tx(&kv_full[slot], C::TILE);
         __syncwarp();
         if (active) {
-          const int first = (j0 + jj) * 128 + my_box * box;
-          tma_load_4d(smem + C::KV_OFF + slot * C::TILE + off, is_v ? &tm_v : &tm_k, &kv_full[slot], my_half * 64,
-                      first & ((1 << p.map.page_shift) - 1), kvh, id);
+          const int first = ((j0 + jj) * 128 + my_box * box) & ((1 << p.map.page_shift) - 1);  // row in its page
+          load_rows(smem + C::KV_OFF + slot * C::TILE + my_box * box * D * 2, is_v ? &tm_v : &tm_k, &kv_full[slot],
+                    ((kvh << p.map.page_shift) + first) >> 3, id);
         }
         ++fill;
       };
@@ -176,8 +175,11 @@ __global__ void __launch_bounds__(768, 1)
       constexpr uint32_t IDESC_QK = make_idesc(128, 128, BF16, false, false);
       constexpr uint32_t IDESC_PV = make_idesc(128, D, BF16, false, true);
       const uint64_t dq_base = make_sdesc(sq, 16, 1024);
-      const uint64_t dk_base = make_sdesc(skv, 16, 1024);
-      const uint64_t dv_base = make_sdesc(skv, C::CHUNK, 1024);
+      // K and V tiles are [8-row group][half][8][128 bytes] (load_rows): 8-row
+      // groups GROUP apart, the second 64 columns 1 KB behind the first
+      constexpr uint32_t GROUP = D * 16;
+      const uint64_t dk_base = make_sdesc(skv, 16, GROUP);      // K-major
+      const uint64_t dv_base = make_sdesc(skv, 1024, GROUP);    // MN-major
       bool ok = true;
       int fill = 0;
       auto take = [&](uint32_t& slot) {
@@ -191,14 +193,14 @@ __global__ void __launch_bounds__(768, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss_e(d, desc_add(a, (kk >> 2) * C::CHUNK + (kk & 3) * 32),
-                   desc_add(bb, (kk >> 2) * C::CHUNK + (kk & 3) * 32), IDESC_QK, kk > 0 ? 1u : 0u, e);
+                   desc_add(bb, (kk >> 2) * 1024 + (kk & 3) * 32), IDESC_QK, kk > 0 ? 1u : 0u, e);
       };
       auto pv = [&](int t, int h, uint32_t vslot, uint32_t acc) {
-        const uint64_t bb = desc_add(dv_base, vslot * C::TILE + h * 8192);
+        const uint64_t bb = desc_add(dv_base, vslot * C::TILE + h * 8 * GROUP);
         const uint32_t d = tmem + C::TM_O + D * t, pa = tmem + C::TM_S + 128 * t + 32 * h;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_e(d, pa + kk * 8, desc_add(bb, kk * 2048), IDESC_PV, kk > 0 ? 1u : acc, e);
+          mma_ts_e(d, pa + kk * 8, desc_add(bb, kk * 2 * GROUP), IDESC_PV, kk > 0 ? 1u : acc, e);
       };
       uint32_t ks;
       take(ks);
