@@ -192,7 +192,8 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
     if (e != cudaSuccess) return from_cuda(e);
     g_launches.fetch_add(1);
   }
-  if (tiles == 1) return FA_OK;  // a unit of one tile is never cut
+  // units that are never cut: of one tile, or all of them short and on an SM of their own
+  if (tiles == 1 || (tiles <= fa::kWholeTiles && (long long)p.B * p.Hkv <= a.grid)) return FA_OK;
   return launch_after(fa::paged_merge_kernel<D, BF16>, dim3(a.grid, p.G), 128, 0, st, a);
 }
 

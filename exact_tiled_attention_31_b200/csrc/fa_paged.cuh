@@ -180,13 +180,12 @@ __device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int 
   if (lane == 0) p.lse[row] = r.w > 0.f ? (r.m + __log2f(r.w)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The shared rows' parts s = first, first + step, ... of a row, eight parts'
+// The shared rows' parts s = first, first + step, ... of a row, FLY parts'
 // loads in flight (one part at a time took a memory latency each: 16 us a unit
 // with 16 parts).
-template <int VEC>
+template <int VEC, int FLY>
 __device__ __forceinline__ void add_shared(const PagedParams& p, size_t row, int D, int lane, int first, int step,
                                            RowSum<VEC>& sum) {
-  constexpr int FLY = 8;
   const size_t rows = (size_t)p.B * p.Hq;
   for (int s = first; s < p.n_pre; s += FLY * step) {
     float l2[FLY], x[FLY][VEC];
@@ -201,6 +200,15 @@ __device__ __forceinline__ void add_shared(const PagedParams& p, size_t row, int
     for (int k = 0; k < FLY; ++k) sum.add(l2[k], x[k]);
   }
 }
+
+// What beginning and ending a unit costs, in tiles (measured with one-tile
+// units: about 2.8 us, against 0.7 us for a tile at an SM's share of HBM).
+// Runs are cut at equal cost, so that a CTA with many short sequences is not
+// the last; the cost lies in front of the unit's first tile.
+constexpr int kUnitCost = 4;
+// Where every unit is at most this many tiles and has an SM to itself, no unit
+// is cut: a CTA takes eight tiles in less time than the merge of parts costs.
+constexpr int kWholeTiles = 8;
 
 // A place in the list of tiles: (sequence, KV head) units in order, each of
 // its sequence's tiles.  A sequence without rows of its own still has one
@@ -229,7 +237,8 @@ __global__ void __launch_bounds__(288, 1)
   constexpr int VEC = D / 32;
   extern __shared__ uint8_t dsm_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
-  __shared__ long long warp_sum[C::WARPS], s_first;  // tiles before the first sequence of this run
+  __shared__ int warp_max[C::WARPS];
+  __shared__ long long warp_sum[C::WARPS], s_first;  // cost before the first sequence of this run
   __shared__ int s_b;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
   float* scratch = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
@@ -249,38 +258,48 @@ __global__ void __launch_bounds__(288, 1)
   }
   pdl_launch();
 
-  // ---- this CTA's run [t0, t1) of the Hkv * sum_b tiles(b) tiles
-  auto tiles_of = [&](int b) {
+  // ---- this CTA's run [t0, t1) of the cost Hkv * sum_b (tiles(b) + kUnitCost)
+  auto cost_of = [&](int b) {
     const int end = min(max(p.seq_lens[b], 0), p.map.max_len);
-    return max(1, (end - p.start + C::KT - 1) / C::KT);
+    return max(1, (end - p.start + C::KT - 1) / C::KT) + kUnitCost;
   };
   const int chunk = (p.B + 255) / 256;
   const int b_lo = min((int)threadIdx.x * chunk, p.B), b_hi = threadIdx.x < 256 ? min(b_lo + chunk, p.B) : b_lo;
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b);
+  int most = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = cost_of(b);
+    mine += n;
+    most = max(most, n);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (warp < C::WARPS && lane == 31) warp_sum[warp] = incl;
+  if (warp < C::WARPS && lane == 31) {
+    warp_sum[warp] = incl;
+    warp_max[warp] = most;
+  }
   __syncthreads();
   long long total = 0, before = incl - mine;
 #pragma unroll
   for (int w = 0; w < C::WARPS; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
+    most = max(most, warp_max[w]);
   }
   total *= p.Hkv;
-  // with fewer tiles than CTAs the last CTAs have none, so that no CTA inside a
-  // unit's range is without a part
+  // tile k of a unit sits kUnitCost + k behind the unit's start.  At most as
+  // many runs as there is cost, so that no run inside a unit is without a tile
   const int runs = (int)min((long long)p.grid, total);
   const long long t0 = c < runs ? c * total / runs : 0, t1 = c < runs ? (c + 1) * total / runs : 0;
   if (threadIdx.x < 256 && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
     int b = b_lo;
     for (; b < b_hi - 1; ++b) {
-      const int n = tiles_of(b);
+      const int n = cost_of(b);
       if (t0 < (before + n) * p.Hkv) break;
       before += n;
     }
@@ -289,11 +308,23 @@ __global__ void __launch_bounds__(288, 1)
   }
   __syncthreads();
   PagedWalk at;
-  at.b = s_b;
+  const long long units = (long long)p.B * p.Hkv;
+  const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA
+  at.b = whole ? min(c / p.Hkv, p.B - 1) : s_b;
   at.load(p, C::KT);
-  at.kvh = (int)((t0 - s_first) / at.tiles);
-  at.tile = (int)((t0 - s_first) % at.tiles);
-  long long left = t1 - t0;
+  const int cost = at.tiles + kUnitCost;
+  at.kvh = (int)((t0 - s_first) / cost);
+  int off = (int)((t0 - s_first) % cost);  // into the unit
+  at.tile = max(0, off - kUnitCost);
+  long long left = t1 - t0;  // cost of what is left of the run
+  if (off < kUnitCost) {     // what is left of the unit's own cost lies in front of its tile 0
+    left -= kUnitCost - off;
+  }
+  if (whole) {
+    at.kvh = c % p.Hkv;
+    at.tile = 0;
+    left = c < units ? at.tiles : 0;
+  }
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- producer
@@ -336,7 +367,7 @@ __global__ void __launch_bounds__(288, 1)
         }
         ids = ids_next;
       }
-      left -= n;
+      left -= n + kUnitCost;  // the next unit's own cost too
       if (left > 0) at.next_unit(p, C::KT);
     }
     // no copy may still be on its way into shared memory when the CTA ends
@@ -354,20 +385,34 @@ __global__ void __launch_bounds__(288, 1)
   uint32_t it = 0;
   bool ok = true, waited = false;
   PagedCut cut{-1, 0, 0, 0};
-  while (left > 0) {
-    const int n = (int)min((long long)(at.tiles - at.tile), left);
-    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
-    // Q^T as the B operand: column lane / 4 of each 8 is a query row
-    uint32_t qb[NB][D / 16][2];
+  // Q^T as the B operand: column lane / 4 of each 8 is a query row
+  uint32_t qb[NB][D / 16][2], qn[1][D / 16][2];
+  bool have_q = false;
+  auto load_q = [&](size_t q_row, auto& to) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int nb = 0; nb < (int)(sizeof(to) / sizeof(to[0])); ++nb) {
       const int r = 8 * nb + (lane >> 2);
       const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (q_row + r) * D) + (lane & 3);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        qb[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
-        qb[nb][kk][1] = r < p.G ? q[8 * kk + 4] : 0u;
+        to[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
+        to[nb][kk][1] = r < p.G ? q[8 * kk + 4] : 0u;
       }
+    }
+  };
+  while (left > 0) {
+    const int n = (int)min((long long)(at.tiles - at.tile), left);
+    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
+    if (NB == 2 || !have_q) load_q(q_row, qb);
+    else {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) qb[0][kk][0] = qn[0][kk][0], qb[0][kk][1] = qn[0][kk][1];
+    }
+    // the next unit's queries follow these in memory: on their way while this
+    // unit streams (for the larger groups the registers do not suffice)
+    if constexpr (NB == 1) {
+      have_q = q_row + p.G < (size_t)p.B * p.Hq;
+      if (have_q) load_q(q_row + p.G, qn);
     }
     float oacc[D / 16][NB][4];
 #pragma unroll
@@ -537,7 +582,7 @@ __global__ void __launch_bounds__(288, 1)
         RowSum<VEC> sum;
         sum.add(l2, acc);
         const size_t row = q_row + r;
-        add_shared<VEC>(p, row, D, lane, 0, 1, sum);
+        add_shared<VEC, NB == 1 ? 8 : 4>(p, row, D, lane, 0, 1, sum);
         store_row<VEC, BF16>(p, row, D, lane, sum);
       } else {
         const size_t slot = (size_t)(2 * c + (begins ? 1 : 0)) * p.G + r;
@@ -552,8 +597,7 @@ __global__ void __launch_bounds__(288, 1)
       cut = PagedCut{at.b, at.kvh, (int)(((x + 1) * runs - 1) / total), 0};
     }
     named_sync(1, 256);  // the scratch is read before the next unit writes it
-    left -= n;
-    at.tile += n;
+    left -= n + kUnitCost;
     if (left > 0) at.next_unit(p, C::KT);
   }
   if (threadIdx.x == 0) p.cuts[c] = cut;
@@ -582,7 +626,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     load_vec<VEC>(p.o_part + slot * D + VEC * lane, x);
     sum.add(p.lse_part[slot], x);
   }
-  add_shared<VEC>(p, row, D, lane, warp, 4, sum);
+  add_shared<VEC, 8>(p, row, D, lane, warp, 4, sum);
   store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
   if (lane == 0) s_m[warp] = sum.m, s_w[warp] = sum.w;
   __syncthreads();
