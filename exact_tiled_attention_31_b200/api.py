@@ -20,7 +20,6 @@ is no fallback.  If ``libfa.so`` is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -470,76 +469,112 @@ def decode(q, k_cache, v_cache, seq_lens, scale: float | None = None, n_splits: 
 
 
 # ---- rotary positions and the paged cache
+#
+# A decode step is a few microseconds on the GPU, so its checks must not cost
+# more: everything about a call that follows from the layout of its tensors
+# (dtype, device, shape, strides) is checked and worked out once per layout.
+# What is kept are sizes and strides: no tensor and no address.
+
+_layouts: dict = {}
+
+
+def _known(key, make, *args):
+    got = _layouts.get(key)
+    if got is None:
+        if len(_layouts) >= 1024:
+            _layouts.clear()
+        got = _layouts[key] = make(*args)
+    return got
+
+
+def _sig(t):
+    return None if t is None else (t.dtype, t.get_device(), t.shape, t.stride())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
 
 def _same_device(first, *ts):
-    """Every given tensor on ``first``'s CUDA device; returns the device."""
-    dev = first.device
-    if dev.type != "cuda":
+    """Every given tensor on ``first``'s CUDA device; returns its index."""
+    if not first.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors must share one device: {t.device} != {dev}")
-    return dev
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors must share one device: {t.device} != {first.device}")
+    return first.get_device()
 
 
-@contextlib.contextmanager
-def _place(device, stream):
-    """Make ``device`` current and, if a stream is given, that stream too, so
-    that what is allocated inside belongs to the stream the kernels run on.
-    Yields the raw stream."""
+def _on(device, stream, call):
+    """``call(raw stream)`` with ``device`` current, and on ``stream`` if one
+    is given, so that what is allocated inside belongs to the stream that the
+    kernels run on."""
     import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-            return
-        if not hasattr(stream, "cuda_stream"):
-            raw = int(stream)
-            stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    if stream is None:
+        if torch.cuda.current_device() == device:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream(device).cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _int32(t, what, shape=None):
     import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
+    if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{what} must be a contiguous CUDA int32 tensor" + (f" of shape {list(shape)}" if shape else ""))
-    return t.data_ptr()
 
 
-def _strides(x, dims, out=False):
-    """The strides of ``dims`` of x (0 for dimensions of one element), rows contiguous."""
-    size, st = x.shape, x.stride()
-    if st[-1] != 1 and size[-1] > 1:
+def _contiguous(shape):
+    st, n = [], 1
+    for s in reversed(shape):
+        st.append(n)
+        n *= s
+    return tuple(reversed(st))
+
+
+def _row_strides(shape, strides, dims, out=False):
+    """The strides of ``dims`` (0 for dimensions of one element), rows contiguous."""
+    if strides[-1] != 1:
         raise ValueError("rows must be contiguous in the last dimension")
     got = []
     for d in dims:
-        s = st[d] if size[d] > 1 else 0
-        if s % 8 or (out and s == 0 and size[d] > 1):
+        s = strides[d] if shape[d] > 1 else 0
+        if s % 8 or (out and s == 0 and shape[d] > 1):
             raise ValueError("strides must be multiples of 8 elements" + (" and not zero in an output" if out else ""))
         got.append(s)
     return got
 
 
-def _extent(x):
-    """The bytes from an empty-free tensor's first element to behind its last."""
-    return x.data_ptr(), x.data_ptr() + x.element_size() * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride())))
+def _rows_layout(x, y, order):
+    """Of rows x and where they go, y (None: a new contiguous tensor): what
+    fa_rows says behind the pointer, for both, and what _apart needs.
+    ``order``: the dimensions of batch (or None), heads and tokens."""
+    if y is not None and (y.shape != x.shape or y.dtype != x.dtype):
+        raise ValueError(f"output {tuple(y.shape)} {y.dtype} does not match {tuple(x.shape)} {x.dtype}")
+    heads, said, size = x.shape[order[1]], [], []
+    for st, out in ((x.stride(), False), (_contiguous(x.shape) if y is None else y.stride(), True)):
+        s = _row_strides(x.shape, st, [d for d in order if d is not None], out)
+        said.append((*(s if order[0] is not None else (0, *s)), heads))
+        size.append(2 * (1 + sum((n - 1) * k for n, k in zip(x.shape, st))) if x.numel() else 0)
+    return (*said, *size, y is not None and y.stride() == x.stride())
 
 
-def _check_rows_out(x, y, what):
-    """An output for the rows of ``x``: x itself, or apart from it."""
-    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
-        raise ValueError(f"{what}: shape {tuple(y.shape)} {y.dtype} does not match {tuple(x.shape)} {x.dtype}")
-    if y.numel() and (y.data_ptr() != x.data_ptr() or y.stride() != x.stride()):
-        (a, b), (c, d) = _extent(x), _extent(y)
-        if a < d and c < b:
-            raise ValueError(f"{what} overlaps its input without being it")
+def _apart(x, y, layout):
+    """An output is its input, in place, or apart from it."""
+    _, _, nx, ny, same = layout
+    if not (same and x == y) and x < y + ny and y < x + nx:
+        raise ValueError("an output overlaps its input without being it")
 
 
-def _check_freqs(freqs, D):
+def _check_freqs(freqs):
     import torch
-    if freqs.dtype != torch.float64 or not freqs.is_cuda or not freqs.is_contiguous() or freqs.dim() != 1:
+    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() != 1:
         raise ValueError("freqs must be a contiguous CUDA float64 tensor of rot_dim / 2 radians per position")
     return 2 * freqs.shape[0]
 
@@ -562,26 +597,23 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
     return torch.tensor(list(out), dtype=torch.float64).to(device), amp.value
 
 
-def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, backward):
+def _rope_layout(q, k, freqs, positions, cu_seqlens, outs):
     import torch
-    xs = (q,) if k is None else (q, k)
+    dev = _same_device(q, k, freqs, positions, cu_seqlens, *outs)
     packed = q.dim() == 3
     if not packed and q.dim() != 4:
         raise ValueError("q must be [B, H, S, D], or packed [H, T, D]")
-    D = q.shape[-1]
-    tokens = q.shape[1:2] if packed else (q.shape[0], q.shape[2])
-    for x in xs:
-        if x.dtype != q.dtype or x.dim() != q.dim() or x.shape[-1] != D or \
-                (x.shape[1:2] if packed else (x.shape[0], x.shape[2])) != tokens:
-            raise ValueError(f"k {tuple(x.shape)} {x.dtype} does not match q {tuple(q.shape)} {q.dtype}")
-    dt, dev = _dt(q), _same_device(q, k, freqs, positions, cu_seqlens)
-    rot = _check_freqs(freqs, D)
-    B, S = (1, tokens[0]) if packed else tokens
-    pos, pos_stride, cu, nseq = None, 0, None, 0
+    order = (None, 0, 1) if packed else (0, 1, 2)
+    B, S = (1, q.shape[1]) if packed else (q.shape[0], q.shape[2])
+    if k is not None and (k.dtype != q.dtype or k.dim() != q.dim() or
+                          any(a != b for d, (a, b) in enumerate(zip(k.shape, q.shape)) if d != order[1])):
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype} does not match q {tuple(q.shape)} {q.dtype}")
+    nseq = pos_stride = 0
     if cu_seqlens is not None:
         if not packed:
             raise ValueError("cu_seqlens goes with packed [H, T, D] tensors")
-        cu, nseq = _int32(cu_seqlens, "cu_seqlens"), cu_seqlens.numel() - 1
+        _int32(cu_seqlens, "cu_seqlens")
+        nseq = cu_seqlens.numel() - 1
         if nseq < 0:
             raise ValueError("cu_seqlens must hold at least one offset")
     if positions is not None:
@@ -589,39 +621,48 @@ def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, bac
                 (positions.dim() == 2 and positions.shape[0] not in (1, B)) or \
                 (S > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions must be a CUDA int32 tensor of shape [{S}] or [{B}, {S}]")
-        pos = positions.data_ptr()
         pos_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
-    elif packed and cu is None:
+    elif packed and cu_seqlens is None:
         raise ValueError("packed tensors need cu_seqlens or positions")
+    rows = [_rows_layout(x, y, order) for x, y in zip((q, k), outs) if x is not None]
+    empty = q.numel() == 0 and (k is None or k.numel() == 0)
+    return dev, _dt(q), _check_freqs(freqs), B, S, q.shape[-1], nseq, pos_stride, rows, empty
+
+
+def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, backward):
+    import torch
+    q_out, k_out = (None, None) if out is None else (out, None) if isinstance(out, torch.Tensor) else out
+    if out is not None and (q_out is None or (k is None) != (k_out is None)):
+        raise ValueError("out must give a tensor for each input")
+    dev, dt, rot, B, S, D, nseq, pos_stride, rows, empty = _known(
+        ("rope", _sig(q), _sig(k), _sig(freqs), _sig(positions), _sig(cu_seqlens), _sig(q_out), _sig(k_out)),
+        _rope_layout, q, k, freqs, positions, cu_seqlens, (q_out, k_out))
 
     def call(raw):
-        ys = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in xs) if out is None else \
-            (out,) if isinstance(out, torch.Tensor) else tuple(y for y in out if y is not None)
-        if len(ys) != len(xs):
-            raise ValueError("out must give a tensor for each input")
-        dims = (1, 0) if packed else (0, 1, 2)
-        rows = [], []
-        for i, (x, y) in enumerate(zip(xs, ys)):
-            if out is not None:
-                _check_rows_out(x, y, "out")
-            if i and ys[0].numel() and y.data_ptr() == ys[0].data_ptr():
-                raise ValueError("the two outputs are the same memory")
-            heads = x.shape[0] if packed else x.shape[1]
-            for t, to, is_out in ((x, rows[0], False), (y, rows[1], True)):
-                b, h, s = _strides(t, (0, 1, 2), is_out) if not packed else (0, *_strides(t, (0, 1), is_out))
-                to.append(_ROWS.pack(t.data_ptr(), b, h, s, heads))
-        if all(x.numel() == 0 for x in xs):
-            return (ys[0], None) if k is None else ys
-        st = fa_rope(b"".join(rows[0]), b"".join(rows[1]), len(xs), freqs.data_ptr(), rot, interleaved, float(amp),
-                     backward, pos, pos_stride, cu, nseq, B, S, D, dt, raw)
-        if st != FA_OK:
-            raise FAError(st, "fa_rope")
-        return (ys[0], None) if k is None else ys
+        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        xp, yp = q.data_ptr(), yq.data_ptr()
+        x, y = _ROWS.pack(xp, *rows[0][0]), _ROWS.pack(yp, *rows[0][1])
+        yk = None
+        if q_out is not None:
+            _apart(xp, yp, rows[0])
+        if k is not None:
+            yk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+            kp, ykp = k.data_ptr(), yk.data_ptr()
+            x += _ROWS.pack(kp, *rows[1][0])
+            y += _ROWS.pack(ykp, *rows[1][1])
+            if k_out is not None:
+                _apart(kp, ykp, rows[1])
+                if ykp == yp and ykp:
+                    raise ValueError("the two outputs are the same memory")
+        if not empty:
+            st = _lib.fa_rope(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions),
+                              pos_stride, _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
+            if st != FA_OK:
+                raise FAError(st, "fa_rope")
+        return yq, yk
 
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with _place(dev, stream) as raw:
-        return call(raw)
+    load_library()
+    return _on(dev, stream, call)
 
 
 def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved: bool = False, amp: float = 1.0, out=None,
@@ -643,28 +684,62 @@ def rope_backward(dq, dk, freqs, positions=None, cu_seqlens=None, interleaved: b
     return _rope(dq, dk, freqs, positions, cu_seqlens, interleaved, amp, out, stream, True)
 
 
-def _pages(k_pages, v_pages, block_table, B, dtype, D):
-    """The bytes of the fa_pages of these tensors, and the number of KV heads."""
+def _pages_layout(k_pages, v_pages, block_table, B, dtype, D):
+    """What fa_pages says of these tensors: (page stride, row stride of the
+    table, n_pages, page_size, heads, max_pages)."""
     import torch
     if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != dtype or v_pages.dtype != dtype:
         raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, D] of the queries' dtype")
     n, heads, page, Dk = k_pages.shape
     if Dk != D:
         raise ValueError(f"pages of D = {Dk} do not match D = {D}")
-    inner, strides = (page * D, D, 1), []
+    strides = []
     for x in (k_pages, v_pages):
-        st = x.stride()
-        if st[1:] != inner and not (n and x[0].is_contiguous()):
+        if n and not x[0].is_contiguous():
             raise ValueError("each page must be contiguous")
-        strides.append(st[0] if n > 1 else heads * page * D)
+        strides.append(x.stride(0) if n > 1 else heads * page * D)
     if strides[0] != strides[1]:
         raise ValueError("k_pages and v_pages must have the same stride from page to page")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or \
             (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError(f"block_table must be a CUDA int32 tensor of shape [{B}, max_pages]")
-    row = block_table.stride(0) if B > 1 else 0
-    return _PAGES.pack(k_pages.data_ptr(), v_pages.data_ptr(), strides[0], block_table.data_ptr(), row, n, page, heads,
-                       block_table.shape[1]), heads
+    return strides[0], block_table.stride(0) if B > 1 else 0, n, page, heads, block_table.shape[1]
+
+
+def _pack_pages(k_pages, v_pages, block_table, layout):
+    return _PAGES.pack(k_pages.data_ptr(), v_pages.data_ptr(), layout[0], block_table.data_ptr(), *layout[1:])
+
+
+def _append_layout(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out):
+    dev = _same_device(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
+    dt = _dt(k)
+    if k.dim() != 3 or k.shape != v.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be equal in shape and dtype: [B, Hkv, D], or packed [Hkv, T, D]")
+    one, D = cu_seqlens is None, k.shape[-1]
+    order = (None, 1, 0) if one else (None, 0, 1)
+    T = k.shape[order[2]]
+    B = T if one else cu_seqlens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must hold at least one offset")
+    pages = _pages_layout(k_pages, v_pages, block_table, B, k.dtype, D)
+    if k.shape[order[1]] != pages[4]:
+        raise ValueError(f"k has {k.shape[order[1]]} heads, the pages {pages[4]}")
+    _int32(seq_lens, "seq_lens", (B,))
+    if not one:
+        _int32(cu_seqlens, "cu_seqlens")
+    if positions is not None:
+        _int32(positions, "positions", (T,))
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
+    q_rows = None
+    if q is not None:
+        if freqs is None:
+            raise ValueError("q is only rotated: it takes freqs")
+        if q.dim() != 3 or q.dtype != k.dtype or q.shape[order[2]] != T or q.shape[-1] != D:
+            raise ValueError(f"q {tuple(q.shape)} {q.dtype} does not match k {tuple(k.shape)} {k.dtype}")
+        q_rows = _rows_layout(q, q_out, order)
+    k_rows, v_rows = ((0, *_row_strides(x.shape, x.stride(), order[1:]), x.shape[order[1]]) for x in (k, v))
+    return dev, dt, B, T, D, pages, k_rows, v_rows, q_rows, 0 if freqs is None else _check_freqs(freqs)
 
 
 def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, q=None, freqs=None, positions=None,
@@ -681,69 +756,45 @@ def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
     the table or a page outside the pool is reported by
     ``check_device_error``."""
     import torch
-    dev = _same_device(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
-    dt = _dt(k)
-    if k.dim() != 3 or k.shape != v.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be equal in shape and dtype: [B, Hkv, D], or packed [Hkv, T, D]")
-    one, D = cu_seqlens is None, k.shape[-1]
-    ht = (1, 0) if one else (0, 1)  # the dimensions of heads and tokens
-    T = k.shape[ht[1]]
-    B = T if one else cu_seqlens.numel() - 1
-    if B < 0:
-        raise ValueError("cu_seqlens must hold at least one offset")
-    pages, heads = _pages(k_pages, v_pages, block_table, B, k.dtype, D)
-    if k.shape[ht[0]] != heads:
-        raise ValueError(f"k has {k.shape[ht[0]]} heads, the pages {heads}")
-    lens = _int32(seq_lens, "seq_lens", (B,))
-    cu = None if one else _int32(cu_seqlens, "cu_seqlens")
-    pos = None if positions is None else _int32(positions, "positions", (T,))
-    rot = 0 if freqs is None else _check_freqs(freqs, D)
-    if q is None and q_out is not None:
-        raise ValueError("q_out goes with q")
-    if q is not None:
-        if freqs is None:
-            raise ValueError("q is only rotated: it takes freqs")
-        if q.dim() != 3 or q.dtype != k.dtype or q.shape[ht[1]] != T or q.shape[-1] != D:
-            raise ValueError(f"q {tuple(q.shape)} {q.dtype} does not match k {tuple(k.shape)} {k.dtype}")
+    dev, dt, B, T, D, pages, k_rows, v_rows, q_rows, rot = _known(
+        ("append", _sig(k), _sig(v), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), _sig(cu_seqlens),
+         _sig(q), _sig(freqs), _sig(positions), _sig(q_out)),
+        _append_layout, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
 
     def call(raw):
-        to = torch.empty(q.shape, dtype=q.dtype, device=dev) if q is not None and q_out is None else q_out
-        if q_out is not None:
-            _check_rows_out(q, q_out, "q_out")
-
-        def rows(x, out=False):
-            h, t = _strides(x, ht, out)
-            return _ROWS.pack(x.data_ptr(), 0, h, t, x.shape[ht[0]])
-
-        if T == 0 or B == 0:
-            return to
-        st = fa_append_paged(rows(k), rows(v), None if q is None else rows(q), None if q is None else rows(to, True),
-                             pages, lens, cu, B, T, None if freqs is None else freqs.data_ptr(), rot, interleaved,
-                             float(amp), pos, D, dt, raw)
-        if st != FA_OK:
-            raise FAError(st, "fa_append_paged")
+        to, qx, qy = q_out, None, None
+        if q is not None:
+            if q_out is None:
+                to = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            xp, yp = q.data_ptr(), to.data_ptr()
+            if q_out is not None:
+                _apart(xp, yp, q_rows)
+            qx, qy = _ROWS.pack(xp, *q_rows[0]), _ROWS.pack(yp, *q_rows[1])
+        if T and B:
+            st = _lib.fa_append_paged(_ROWS.pack(k.data_ptr(), *k_rows), _ROWS.pack(v.data_ptr(), *v_rows), qx, qy,
+                                      _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(),
+                                      _ptr(cu_seqlens), B, T, _ptr(freqs), rot, interleaved, amp, _ptr(positions), D,
+                                      dt, raw)
+            if st != FA_OK:
+                raise FAError(st, "fa_append_paged")
         return to
 
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with _place(dev, stream) as raw:
-        return call(raw)
+    load_library()
+    return _on(dev, stream, call)
 
 
-def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, out, lse, workspace,
-                  stream):
+def _decode_layout(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, out, lse, workspace):
     import torch
     dev = _same_device(q, k_pages, v_pages, block_table, seq_lens, prefix_table, out, lse, workspace)
     dt = _dt(q)
     if q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B, Hq, D] tensor")
     B, Hq, D = q.shape
-    pages, heads = _pages(k_pages, v_pages, block_table, B, q.dtype, D)
-    lens = _int32(seq_lens, "seq_lens", (B,))
-    table = None
+    pages = _pages_layout(k_pages, v_pages, block_table, B, q.dtype, D)
+    _int32(seq_lens, "seq_lens", (B,))
     if prefix_table is not None:
-        table = _int32(prefix_table, "prefix_table")
-        if prefix_table.dim() != 1 or prefix_table.shape[0] * k_pages.shape[2] < prefix_len:
+        _int32(prefix_table, "prefix_table")
+        if prefix_table.dim() != 1 or prefix_table.shape[0] * pages[3] < prefix_len:
             raise ValueError(f"prefix_table must name the pages of {prefix_len} rows")
     if out is not None:
         _check((out,), q.shape)
@@ -751,30 +802,41 @@ def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix
             raise TypeError("out must have q's dtype")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous fp32 tensor of shape [{B}, {Hq}]")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    with torch.cuda.device(dev):  # the size is that of the device
+        need = fa_decode_prefix_workspace_size(B, Hq, pages[4], prefix_len, D)
+    size = need if workspace is None else workspace.numel() * workspace.element_size()
+    return dev, dt, B, Hq, D, pages, need, size
+
+
+def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, out, lse, workspace,
+                  stream):
+    import torch
+    dev, dt, B, Hq, D, pages, need, size = _known(
+        ("decode", _sig(q), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), prefix_len,
+         _sig(prefix_table), _sig(out), _sig(lse), _sig(workspace)),
+        _decode_layout, q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, out, lse, workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
 
     def call(raw):
         o = torch.empty_like(q) if out is None else out
-        ll = torch.empty((B, Hq), device=dev, dtype=torch.float32) if lse is None else lse
-        ws = workspace
-        if ws is None:
-            need = fa_decode_prefix_workspace_size(B, Hq, heads, prefix_len, D)
-            ws = torch.empty(max(need, 1), device=dev, dtype=torch.uint8)
-        size = ws.numel() * ws.element_size()
+        ll = torch.empty((B, Hq), device=q.device, dtype=torch.float32) if lse is None else lse
+        ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8) if workspace is None else workspace
+        at = _pack_pages(k_pages, v_pages, block_table, pages)
         if prefix_len:
-            st = fa_decode_prefix(q.data_ptr(), pages, lens, prefix_len, table, o.data_ptr(), ll.data_ptr(), B, Hq, D,
-                                  scale, dt, ws.data_ptr(), size, raw)
+            st = _lib.fa_decode_prefix(q.data_ptr(), at, seq_lens.data_ptr(), prefix_len, _ptr(prefix_table),
+                                       o.data_ptr(), ll.data_ptr(), B, Hq, D, scale, dt, ws.data_ptr(), size, raw)
         else:
-            st = fa_decode_paged(q.data_ptr(), pages, lens, o.data_ptr(), ll.data_ptr(), B, Hq, D, scale, dt,
-                                 ws.data_ptr(), size, raw)
+            st = _lib.fa_decode_paged(q.data_ptr(), at, seq_lens.data_ptr(), o.data_ptr(), ll.data_ptr(), B, Hq, D,
+                                      scale, dt, ws.data_ptr(), size, raw)
         if st != FA_OK:
             raise FAError(st, "fa_decode_prefix" if prefix_len else "fa_decode_paged")
         return o, ll
 
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with _place(dev, stream) as raw:
-        return call(raw)
+    load_library()
+    return _on(dev, stream, call)
 
 
 def decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float | None = None, out=None, lse=None,

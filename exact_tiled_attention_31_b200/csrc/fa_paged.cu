@@ -44,6 +44,25 @@ int log2_of(int x) {
   return s;
 }
 
+// A launch that may begin before the kernel ahead of it on the stream ends;
+// every kernel here waits (pdl_wait) before it touches memory.
+template <typename... A>
+fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  return from_cuda(e);
+}
+
 // ---------------------------------------------------------------- rotary positions
 // Heads a block walks over: all of them share a token's sines and cosines, but
 // below about eight blocks per SM a block takes fewer, down to one batch of
@@ -65,10 +84,8 @@ fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
   p.per = heads_per_block(blocks, heads);
   const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
   if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
-  if (inter) fa::rope_kernel<D, BF16, true><<<grid, fa::kRopeThreads, 0, st>>>(p);
-  else fa::rope_kernel<D, BF16, false><<<grid, fa::kRopeThreads, 0, st>>>(p);
-  g_launches.fetch_add(1);
-  return from_cuda(cudaGetLastError());
+  return launch_after(inter ? fa::rope_kernel<D, BF16, true> : fa::rope_kernel<D, BF16, false>, grid, fa::kRopeThreads,
+                      0, st, p);
 }
 
 template <int D, bool BF16>
@@ -79,10 +96,8 @@ fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
   p.per = heads_per_block(blocks, heads);
   const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
   if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
-  if (inter) fa::append_kernel<D, BF16, true><<<grid, fa::kRopeThreads, 0, st>>>(p);
-  else fa::append_kernel<D, BF16, false><<<grid, fa::kRopeThreads, 0, st>>>(p);
-  g_launches.fetch_add(1);
-  return from_cuda(cudaGetLastError());
+  return launch_after(inter ? fa::append_kernel<D, BF16, true> : fa::append_kernel<D, BF16, false>, grid,
+                      fa::kRopeThreads, 0, st, p);
 }
 
 bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0; }
@@ -154,25 +169,6 @@ bool map_queries(CUtensorMap* m, const void* q, int B, int Hkv, int G, int D, bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A launch that may begin before the kernel ahead of it on the stream ends;
-// the kernel itself waits (griddepcontrol.wait) before it reads what that wrote.
-template <typename... A>
-fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e == cudaSuccess) g_launches.fetch_add(1);
-  return from_cuda(e);
-}
-
 template <int D, bool BF16, int NB>
 fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_t st) {
   using C = fa::PagedCfg<D, NB>;
@@ -183,15 +179,8 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
   fa::PagedParams a = p;
   const long long tiles = std::max(1, (p.map.max_len - p.start + C::KT - 1) / C::KT);  // of the longest sequence
   a.grid = (int)std::min<long long>(paged_grid(), (long long)p.B * p.Hkv * tiles);
-  if (p.n_pre) {
-    const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
-    if (s != FA_OK) return s;
-  } else {
-    fa::paged_kernel<D, BF16, NB><<<a.grid, C::THREADS, C::SMEM, st>>>(mk, mv, a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return from_cuda(e);
-    g_launches.fetch_add(1);
-  }
+  const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
+  if (s != FA_OK) return s;
   // units that are never cut: of one tile, or all of them short and on an SM of their own
   if (tiles == 1 || (tiles <= fa::kWholeTiles && (long long)p.B * p.Hkv <= a.grid)) return FA_OK;
   return launch_after(fa::paged_merge_kernel<D, BF16>, dim3(a.grid, p.G), 128, 0, st, a);
@@ -208,10 +197,7 @@ fa_status launch_prefix(const fa::PrefixParams& p, const void* q, const fa_pages
   if (set_smem<fa::prefix_kernel<D, BF16>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
   const long long grid = (long long)p.n_pre * p.n_pairs * p.Hkv;
   if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  fa::prefix_kernel<D, BF16><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) g_launches.fetch_add(1);
-  return from_cuda(e);
+  return launch_after(fa::prefix_kernel<D, BF16>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, mq, mk, mv, p);
 }
 
 template <int D, bool BF16>

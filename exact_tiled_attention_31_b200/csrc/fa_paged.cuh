@@ -121,8 +121,6 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Page of box `first row` of sequence b, or n_pages (out of the pool: TMA
 // fills zeros) with an argument error where the table names none.
@@ -210,6 +208,11 @@ constexpr int kUnitCost = 4;
 // is cut: a CTA takes eight tiles in less time than the merge of parts costs.
 constexpr int kWholeTiles = 8;
 
+// floor(a / b), b > 0, a >= 0: by 32-bit division where both fit
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // A place in the list of tiles: (sequence, KV head) units in order, each of
 // its sequence's tiles.  A sequence without rows of its own still has one
 // (empty) tile, so that its outputs are written.
@@ -256,6 +259,9 @@ __global__ void __launch_bounds__(288, 1)
     s_b = 0;
     s_first = 0;
   }
+  // After prefix_kernel (which has itself waited for all before it) this kernel
+  // runs ahead and waits only where it needs the shared rows' parts.
+  if (!p.n_pre) pdl_wait();
   pdl_launch();
 
   // ---- this CTA's run [t0, t1) of the cost Hkv * sum_b (tiles(b) + kUnitCost)
@@ -295,7 +301,8 @@ __global__ void __launch_bounds__(288, 1)
   // tile k of a unit sits kUnitCost + k behind the unit's start.  At most as
   // many runs as there is cost, so that no run inside a unit is without a tile
   const int runs = (int)min((long long)p.grid, total);
-  const long long t0 = c < runs ? c * total / runs : 0, t1 = c < runs ? (c + 1) * total / runs : 0;
+  const long long t0 = c < runs ? quot(c * total, runs) : 0,
+                  t1 = c < runs ? quot((c + 1) * total, runs) : 0;
   if (threadIdx.x < 256 && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
     int b = b_lo;
     for (; b < b_hi - 1; ++b) {
@@ -313,8 +320,8 @@ __global__ void __launch_bounds__(288, 1)
   at.b = whole ? min(c / p.Hkv, p.B - 1) : s_b;
   at.load(p, C::KT);
   const int cost = at.tiles + kUnitCost;
-  at.kvh = (int)((t0 - s_first) / cost);
-  int off = (int)((t0 - s_first) % cost);  // into the unit
+  at.kvh = (int)quot(t0 - s_first, cost);
+  const int off = (int)(t0 - s_first - (long long)at.kvh * cost);  // into the unit
   at.tile = max(0, off - kUnitCost);
   long long left = t1 - t0;  // cost of what is left of the run
   if (off < kUnitCost) {     // what is left of the unit's own cost lies in front of its tile 0
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(288, 1)
     for (uint32_t f = it > C::STAGES ? it - C::STAGES : 0; f < it; ++f)
       mbar_wait(&full[f % C::STAGES], (f / C::STAGES) & 1, PAGED_SITE_DRAIN);
     __syncwarp();
-    pdl_wait();
+    if (p.n_pre) pdl_wait();
     return;
   }
 
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(288, 1)
         }
       }
     named_sync(1, 256);
-    if (p.n_pre && !waited) {  // the shared rows' parts come from the kernel before
+    if (p.n_pre && !waited) {  // the shared rows' parts
       pdl_wait();
       waited = true;
     }
@@ -594,14 +601,14 @@ __global__ void __launch_bounds__(288, 1)
       // the CTA that runs the unit's last tile x: the largest c' with
       // floor(c' total / runs) <= x
       const long long x = t1 + (at.tiles - at.tile - n) - 1;
-      cut = PagedCut{at.b, at.kvh, (int)(((x + 1) * runs - 1) / total), 0};
+      cut = PagedCut{at.b, at.kvh, (int)quot((x + 1) * runs - 1, total), 0};
     }
     named_sync(1, 256);  // the scratch is read before the next unit writes it
     left -= n + kUnitCost;
     if (left > 0) at.next_unit(p, C::KT);
   }
   if (threadIdx.x == 0) p.cuts[c] = cut;
-  if (!waited) pdl_wait();
+  if (p.n_pre && !waited) pdl_wait();
 }
 
 // The units that a boundary between CTAs cut: block (c, r) joins the parts of
@@ -613,6 +620,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   __shared__ __align__(16) float s_o[4][D];
   __shared__ float s_m[4], s_w[4];
   pdl_wait();
+  pdl_launch();
   const PagedCut cut = p.cuts[blockIdx.x];
   if (cut.b < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;

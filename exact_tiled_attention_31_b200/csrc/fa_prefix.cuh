@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(768, 1)
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
+  pdl_wait();
   pdl_launch();
   tc_fence_before();
   __syncthreads();

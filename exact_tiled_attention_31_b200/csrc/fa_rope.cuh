@@ -110,6 +110,8 @@ struct RopeParams {
 // grid: (token tiles, head groups); block: tokens x D / 16 items
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  pdl_wait();
+  pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
   const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;
@@ -194,6 +196,8 @@ struct AppendParams {
 
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams p) {
+  pdl_wait();
+  pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
   const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;

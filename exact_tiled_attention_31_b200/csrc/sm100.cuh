@@ -421,6 +421,14 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Programmatic dependent launch.  A kernel launched with that attribute may
+// begin before the one ahead of it on the stream ends: pdl_wait() returns once
+// everything ahead has completed and its writes are visible.  pdl_launch(),
+// always after pdl_wait(), lets the kernel behind begin in the same way, so
+// that what is ahead of this kernel is complete for it too.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Named barrier over `count` threads (a multiple of 32).
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
