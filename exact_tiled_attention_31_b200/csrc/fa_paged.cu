@@ -103,8 +103,8 @@ fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
 bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0; }
 
 // ---------------------------------------------------------------- paged decode
-constexpr int kPagedGridMax = 1024;
-int paged_grid() { return std::min(sm_count(), kPagedGridMax); }
+constexpr int kPagedCtas = 3;  // of paged_kernel on an SM, at most
+int paged_grid() { return kPagedCtas * sm_count(); }
 
 // Ranges the shared rows are cut into: units = KV heads x query pairs CTAs run
 // one range each.  The cost of n ranges is waves x (tiles of the longest range
@@ -122,7 +122,7 @@ int prefix_splits(long long units, int P) {
 }
 
 struct PagedWs {
-  size_t cuts, lse_part, o_part, pre_lse, pre_o, total;
+  size_t cuts, lse_part, o_part, pre_lse, pre_o, own_lse, own_o, unit_cut, total;
   int n_pre, n_pairs, per_tile;
 };
 
@@ -133,13 +133,16 @@ PagedWs paged_layout(int B, int Hq, int Hkv, int P, int D) {
   w.per_tile = 128 / G;
   w.n_pairs = (int)(((long long)B + 2 * w.per_tile - 1) / (2 * w.per_tile));
   w.n_pre = P > 0 ? prefix_splits((long long)Hkv * w.n_pairs, P) : 0;
-  const size_t pre = (size_t)w.n_pre * B * Hq;
+  const size_t pre = (size_t)w.n_pre * B * Hq, own = w.n_pre ? (size_t)B * Hq : 0;
   w.cuts = 0;
   w.lse_part = up256(paged_grid() * sizeof(fa::PagedCut));
   w.o_part = w.lse_part + up256(parts * 4);
   w.pre_lse = w.o_part + up256(parts * D * 4);
   w.pre_o = w.pre_lse + up256(pre * 4);
-  w.total = w.pre_o + up256(pre * D * 4);
+  w.own_lse = w.pre_o + up256(pre * D * 4);
+  w.own_o = w.own_lse + up256(own * 4);
+  w.unit_cut = w.own_o + up256(own * D * 4);
+  w.total = w.unit_cut + up256(w.n_pre ? (size_t)B * Hkv * 4 : 0);
   return w;
 }
 
@@ -178,9 +181,12 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
   if (set_smem<fa::paged_kernel<D, BF16, NB>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
   fa::PagedParams a = p;
   const long long tiles = std::max(1, (p.map.max_len - p.start + C::KT - 1) / C::KT);  // of the longest sequence
-  a.grid = (int)std::min<long long>(paged_grid(), (long long)p.B * p.Hkv * tiles);
+  static_assert(C::CTAS <= kPagedCtas, "workspace for every CTA");
+  a.grid = (int)std::min<long long>((long long)C::CTAS * sm_count(), (long long)p.B * p.Hkv * tiles);
   const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
   if (s != FA_OK) return s;
+  if (p.n_pre)
+    return launch_after(fa::paged_join_kernel<D, BF16>, dim3((unsigned)(((long long)p.B * p.Hq + 7) / 8)), 256, 0, st, a);
   // units that are never cut: of one tile, or all of them short and on an SM of their own
   if (tiles == 1 || (tiles <= fa::kWholeTiles && (long long)p.B * p.Hkv <= a.grid)) return FA_OK;
   return launch_after(fa::paged_merge_kernel<D, BF16>, dim3(a.grid, p.G), 128, 0, st, a);
@@ -241,6 +247,9 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   p.lse = lse;
   p.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
   p.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+  p.own_o = reinterpret_cast<float*>(ws + w.own_o);
+  p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
+  p.unit_cut = reinterpret_cast<int*>(ws + w.unit_cut);
   p.n_pre = w.n_pre, p.start = prefix_len;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;

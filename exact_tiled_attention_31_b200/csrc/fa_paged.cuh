@@ -12,20 +12,23 @@
 //
 // Bound: HBM, 4 D bytes a row and KV head, read once.  So the work is dealt
 // out by rows: the tiles of all (sequence, KV head) units, in order, are cut
-// into equal contiguous runs, one per SM, from the lengths on the device: a
-// ragged batch keeps every SM streaming to the end, whatever its lengths.
-// A unit that one run covers whole is finished there; the units cut by a
-// boundary (at most one per CTA) leave normalised fp32 parts that
+// into contiguous runs of equal cost, one per CTA, from the lengths on the
+// device: a ragged batch keeps every SM streaming to the end, whatever its
+// lengths.  A unit that one run covers whole is finished there; the units cut
+// by a boundary (at most one begins in a CTA) leave normalised fp32 parts that
 // paged_merge_kernel joins.
 //
-// Inside a CTA one producer warp fills a ring of stages (a tile's K and V
+// A CTA has one producer warp, which fills a ring of stages (a tile's K and V
 // rows) by TMA, a box per page, and runs ahead of the consumers over unit
-// boundaries, so the stream does not pause when a unit ends.  Eight consumer
-// warps in two groups take alternate tiles, a warp 16 rows of each.  The
-// products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with the
-// cache rows (then the head's columns) as the 16-row side of m16n8k16: a
-// group of up to 8 query heads then pads to 8 instead of 16, and one ldmatrix
-// feeds a whole operand.
+// boundaries; and four consumer warps, each with 16 rows of every tile.  Three
+// CTAs share an SM (two for groups above 8 with D = 128): what a unit costs
+// besides its rows (queries in, four warps' parts joined, a result out: about
+// 2.8 us) is latency, and the other CTAs' streams cover it.  One CTA of eight
+// consumer warps with the same 192 KB in flight took 28 us instead of 21 for 64
+// sequences of up to 512 rows.  The products are formed transposed,
+// S^T = K Q^T and O^T = V^T P^T, with the cache rows (then the head's columns)
+// as the 16-row side of m16n8k16: a group of up to 8 query heads then pads to
+// 8 instead of 16, and one ldmatrix feeds a whole operand.
 #pragma once
 
 #include "fa_decode.cuh"
@@ -53,9 +56,13 @@ struct PagedParams {
   PagedCut* cuts;        // [grid]
   void* o;               // [B, Hq, D]
   float* lse;            // [B, Hq]
-  // parts over the shared rows [0, start) (start = 0: none)
+  // With shared rows [0, start) in front (n_pre > 0) nothing is finished here:
+  // paged_join_kernel joins the shared rows' parts with what this kernel leaves.
   const float* pre_o;    // [n_pre, B * Hq, D]
   const float* pre_lse;  // [n_pre, B * Hq]
+  float* own_o;          // [B * Hq, D] parts of units that are not cut
+  float* own_lse;        // [B * Hq]
+  int* unit_cut;         // [B * Hkv] the CTA that begins a cut unit, or -1
   int n_pre, start;
   int B, Hq, Hkv, G, grid;
   float scale_log2;
@@ -68,18 +75,15 @@ struct PagedCfg {
   static constexpr int GROUP = D * 16;                 // 8 rows: D / 64 swizzle atoms of 1 KB
   static constexpr int TILE = KT * D * 2;              // K or V
   static constexpr int STAGE = 2 * TILE;
-  // 128 to 192 KB in flight.  Even: tiles alternate between the two consumer
-  // groups, so a stage then belongs to one group, which sees every phase of its
-  // barrier.  (With an odd count a group would meet a stage every second phase,
-  // and a wait by parity cannot tell a phase from the one two before it.)
-  static constexpr int STAGES = D == 64 ? 10 : NB == 1 ? 6 : 4;
-  static_assert(STAGES % 2 == 0, "a stage belongs to one consumer group");
-  static constexpr int WARPS = 8;
+  static constexpr int STAGES = (D == 128 ? 3 : 6) - (NB == 2 && D == 128);
+  static constexpr int CTAS = 2;  // per SM
+  static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int OSTR = D + 4;                   // fp32 row stride of the scratch: conflict-free
-  static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats per warp
-  static constexpr uint32_t SMEM = STAGES * STAGE + WARPS * SCRATCH * 4 + 1024;
-  static_assert(SMEM + 256 <= 227 * 1024, "shared memory per block, the barriers and the run's place included");
+  static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats of one warp's part
+  static constexpr uint32_t SMEM = STAGES * STAGE + 2 * SCRATCH * 4 + 1024;
+  // with the barriers and the run's place, and 1 KB that the system takes
+  static_assert(CTAS * (SMEM + 256 + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
@@ -131,23 +135,13 @@ __device__ __forceinline__ int page_of(const PagedMap& m, const int* row, int fi
   return m.n_pages;
 }
 
-// O and LSE of one row from `n` parts and the shared rows' parts: a lane
-// holds VEC columns of the row.
+// A row joined from parts: a lane holds VEC columns of it.
 template <int VEC>
 struct RowSum {
   float m = -INFINITY, w = 0.f, o[VEC];
   __device__ __forceinline__ RowSum() {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) o[i] = 0.f;
-  }
-  // a normalised part of logarithm l2 (log2; -inf: of no rows)
-  __device__ __forceinline__ void add(float l2, const float (&x)[VEC]) {
-    if (l2 == -INFINITY) return;
-    const float mn = fmaxf(m, l2), a = ex2(m - mn), b = ex2(l2 - mn);
-    w = w * a + b;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = o[i] * a + b * x[i];
-    m = mn;
   }
 };
 
@@ -168,45 +162,63 @@ __device__ __forceinline__ void store_vec(float* p, const float (&x)[VEC]) {
   else
     *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
 }
-// the finished row: O in 16 bits, LSE in natural units
+// The n parts s of a row, l2(s) the log2 of each one's sum (-inf: of no rows)
+// and o(s) its normalised columns: the lanes take the logarithms of 32 parts at
+// once, then eight parts' columns are in flight at a time.
+template <int VEC, typename L, typename O>
+__device__ __forceinline__ void add_parts(RowSum<VEC>& sum, int n, int lane, L&& l2, O&& o) {
+  constexpr int FLY = 8;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int k = min(32, n - s0);
+    const float l = lane < k ? l2(s0 + lane) : -INFINITY;
+    float mn = l;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+    mn = fmaxf(mn, sum.m);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float a = ex2(sum.m - base), w = ex2(l - base);
+    float wt = w;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) wt += __shfl_xor_sync(0xffffffffu, wt, d);
+    sum.m = mn;
+    sum.w = sum.w * a + wt;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum.o[i] *= a;
+    for (int j = 0; j < k; j += FLY) {
+      float x[FLY][VEC];
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) load_vec<VEC>(o(s0 + min(j + f, k - 1)) + VEC * lane, x[f]);
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) {
+        const float wf = j + f < k ? __shfl_sync(0xffffffffu, w, j + f) : 0.f;
+        if (wf != 0.f) {  // a part of no rows holds no columns
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sum.o[i] += wf * x[f][i];
+        }
+      }
+    }
+  }
+}
+// the finished row: O in 16 bits, LSE in natural units (a row of nothing: 0
+// and -inf; NaN scores give NaN)
 template <int VEC, bool BF16>
 __device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int D, int lane, const RowSum<VEC>& r) {
-  const float inv = r.w > 0.f ? 1.f / r.w : 0.f;
+  const float inv = r.w == 0.f ? 0.f : 1.f / r.w;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + VEC * lane);
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) dst[i] = pack2<BF16>(r.o[2 * i] * inv, r.o[2 * i + 1] * inv);
-  if (lane == 0) p.lse[row] = r.w > 0.f ? (r.m + __log2f(r.w)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0) p.lse[row] = r.w == 0.f ? -INFINITY : (r.m + __log2f(r.w)) * 0.69314718055994531f;
 }
 
-// The shared rows' parts s = first, first + step, ... of a row, FLY parts'
-// loads in flight (one part at a time took a memory latency each: 16 us a unit
-// with 16 parts).
-template <int VEC, int FLY>
-__device__ __forceinline__ void add_shared(const PagedParams& p, size_t row, int D, int lane, int first, int step,
-                                           RowSum<VEC>& sum) {
-  const size_t rows = (size_t)p.B * p.Hq;
-  for (int s = first; s < p.n_pre; s += FLY * step) {
-    float l2[FLY], x[FLY][VEC];
-#pragma unroll
-    for (int k = 0; k < FLY; ++k) {
-      const size_t pr = (size_t)(s + k * step) * rows + row;
-      const bool in = s + k * step < p.n_pre;
-      l2[k] = in ? p.pre_lse[pr] : -INFINITY;
-      if (in) load_vec<VEC>(p.pre_o + pr * D + VEC * lane, x[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < FLY; ++k) sum.add(l2[k], x[k]);
-  }
-}
-
-// What beginning and ending a unit costs, in tiles (measured with one-tile
-// units: about 2.8 us, against 0.7 us for a tile at an SM's share of HBM).
-// Runs are cut at equal cost, so that a CTA with many short sequences is not
-// the last; the cost lies in front of the unit's first tile.
-constexpr int kUnitCost = 4;
-// Where every unit is at most this many tiles and has an SM to itself, no unit
-// is cut: a CTA takes eight tiles in less time than the merge of parts costs.
+// What beginning and ending a unit costs, in tiles.  Runs are cut at equal
+// cost, so that a CTA with many short sequences is not the last; the cost lies
+// in front of the unit's first tile.
+constexpr int kUnitCost = 2;
+// Where every unit is at most this many tiles and there is a CTA for each, no
+// unit is cut: a CTA takes eight tiles in less time than joining parts costs.
 constexpr int kWholeTiles = 8;
+// Below this cost a run is not worth a CTA and a part.
+constexpr int kMinRun = 4;
 
 // floor(a / b), b > 0, a >= 0: by 32-bit division where both fit
 __device__ __forceinline__ long long quot(long long a, long long b) {
@@ -233,7 +245,7 @@ struct PagedWalk {
 };
 
 template <int D, bool BF16, int NB>
-__global__ void __launch_bounds__(288, 1)
+__global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTAS)
     paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const PagedParams p) {
   using C = PagedCfg<D, NB>;
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(288, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);
+      mbar_init(&empty[s], C::WARPS);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -259,8 +271,8 @@ __global__ void __launch_bounds__(288, 1)
     s_b = 0;
     s_first = 0;
   }
-  // After prefix_kernel (which has itself waited for all before it) this kernel
-  // runs ahead and waits only where it needs the shared rows' parts.
+  // Behind prefix_kernel (which has itself waited for all before it) this kernel
+  // runs ahead: it reads nothing of that one's, and only waits for its end.
   if (!p.n_pre) pdl_wait();
   pdl_launch();
 
@@ -269,8 +281,10 @@ __global__ void __launch_bounds__(288, 1)
     const int end = min(max(p.seq_lens[b], 0), p.map.max_len);
     return max(1, (end - p.start + C::KT - 1) / C::KT) + kUnitCost;
   };
-  const int chunk = (p.B + 255) / 256;
-  const int b_lo = min((int)threadIdx.x * chunk, p.B), b_hi = threadIdx.x < 256 ? min(b_lo + chunk, p.B) : b_lo;
+  constexpr int FIND = 32 * C::WARPS;  // threads that look for the run
+  const int chunk = (p.B + FIND - 1) / FIND;
+  const int b_lo = (int)min((long long)threadIdx.x * chunk, (long long)p.B);
+  const int b_hi = threadIdx.x < FIND ? min(b_lo + chunk, p.B) : b_lo;
   long long mine = 0;
   int most = 0;
   for (int b = b_lo; b < b_hi; ++b) {
@@ -298,12 +312,13 @@ __global__ void __launch_bounds__(288, 1)
     most = max(most, warp_max[w]);
   }
   total *= p.Hkv;
-  // tile k of a unit sits kUnitCost + k behind the unit's start.  At most as
-  // many runs as there is cost, so that no run inside a unit is without a tile
-  const int runs = (int)min((long long)p.grid, total);
+  // Tile k of a unit sits kUnitCost + k behind the unit's start.  At most as
+  // many runs as there is cost, so that no run inside a unit is without a tile.
+  const long long units = (long long)p.B * p.Hkv;
+  const int runs = (int)min((long long)p.grid, max(units, total / kMinRun));
   const long long t0 = c < runs ? quot(c * total, runs) : 0,
                   t1 = c < runs ? quot((c + 1) * total, runs) : 0;
-  if (threadIdx.x < 256 && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
+  if (threadIdx.x < FIND && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
     int b = b_lo;
     for (; b < b_hi - 1; ++b) {
       const int n = cost_of(b);
@@ -315,22 +330,21 @@ __global__ void __launch_bounds__(288, 1)
   }
   __syncthreads();
   PagedWalk at;
-  const long long units = (long long)p.B * p.Hkv;
-  const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA
-  at.b = whole ? min(c / p.Hkv, p.B - 1) : s_b;
-  at.load(p, C::KT);
-  const int cost = at.tiles + kUnitCost;
-  at.kvh = (int)quot(t0 - s_first, cost);
-  const int off = (int)(t0 - s_first - (long long)at.kvh * cost);  // into the unit
-  at.tile = max(0, off - kUnitCost);
-  long long left = t1 - t0;  // cost of what is left of the run
-  if (off < kUnitCost) {     // what is left of the unit's own cost lies in front of its tile 0
-    left -= kUnitCost - off;
-  }
-  if (whole) {
+  long long left;  // cost of what is left of the run, from tile at.tile on
+  if (units <= p.grid && most <= kWholeTiles + kUnitCost) {  // the same in every CTA: a unit each
+    at.b = min(c / p.Hkv, p.B - 1);
+    at.load(p, C::KT);
     at.kvh = c % p.Hkv;
     at.tile = 0;
     left = c < units ? at.tiles : 0;
+  } else {
+    at.b = s_b;
+    at.load(p, C::KT);
+    const int cost = at.tiles + kUnitCost;
+    at.kvh = (int)quot(t0 - s_first, cost);
+    const int off = (int)(t0 - s_first - (long long)at.kvh * cost);  // into the unit
+    at.tile = max(0, off - kUnitCost);
+    left = t1 - t0 - max(0, kUnitCost - off);
   }
 
   if (warp == C::WARPS) {
@@ -386,40 +400,26 @@ __global__ void __launch_bounds__(288, 1)
   }
 
   // ------------------------------------------------------------------ consumers
-  const int grp = warp >> 2, wq = warp & 3;
   const int r0 = 2 * (lane & 3);  // this lane's query rows 8 nb + r0, + 1; its cache rows lane / 4, + 8
-  float* ws = scratch + warp * C::SCRATCH;  // m[ROWS] l[ROWS] lr[ROWS] O[ROWS][OSTR]
+  // one of two parts in the scratch: of warps w and w + 2
+  float* ws = scratch + (warp & 1) * C::SCRATCH;
   uint32_t it = 0;
-  bool ok = true, waited = false;
+  bool ok = true;
   PagedCut cut{-1, 0, 0, 0};
-  // Q^T as the B operand: column lane / 4 of each 8 is a query row
-  uint32_t qb[NB][D / 16][2], qn[1][D / 16][2];
-  bool have_q = false;
-  auto load_q = [&](size_t q_row, auto& to) {
+  while (left > 0) {
+    const int n = (int)min((long long)(at.tiles - at.tile), left);
+    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
+    // Q^T as the B operand: column lane / 4 of each 8 is a query row
+    uint32_t qb[NB][D / 16][2];
 #pragma unroll
-    for (int nb = 0; nb < (int)(sizeof(to) / sizeof(to[0])); ++nb) {
+    for (int nb = 0; nb < NB; ++nb) {
       const int r = 8 * nb + (lane >> 2);
       const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (q_row + r) * D) + (lane & 3);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        to[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
-        to[nb][kk][1] = r < p.G ? q[8 * kk + 4] : 0u;
+        qb[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
+        qb[nb][kk][1] = r < p.G ? q[8 * kk + 4] : 0u;
       }
-    }
-  };
-  while (left > 0) {
-    const int n = (int)min((long long)(at.tiles - at.tile), left);
-    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
-    if (NB == 2 || !have_q) load_q(q_row, qb);
-    else {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) qb[0][kk][0] = qn[0][kk][0], qb[0][kk][1] = qn[0][kk][1];
-    }
-    // the next unit's queries follow these in memory: on their way while this
-    // unit streams (for the larger groups the registers do not suffice)
-    if constexpr (NB == 1) {
-      have_q = q_row + p.G < (size_t)p.B * p.Hq;
-      if (have_q) load_q(q_row + p.G, qn);
     }
     float oacc[D / 16][NB][4];
 #pragma unroll
@@ -433,11 +433,10 @@ __global__ void __launch_bounds__(288, 1)
       for (int e = 0; e < 2; ++e) m[nb][e] = -INFINITY, l[nb][e] = lr[nb][e] = 0.f;
 
     for (int i = 0; i < n; ++i, ++it) {
-      if ((int)(it & 1) != grp) continue;
       const uint32_t st = it % C::STAGES;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / C::STAGES) & 1, PAGED_SITE_FULL));
       if (!ok) continue;  // error recorded: take no more tiles, but keep to the barriers below
-      const int key0 = p.start + (at.tile + i) * C::KT + 16 * wq;  // this warp's 16 rows
+      const int key0 = p.start + (at.tile + i) * C::KT + 16 * warp;  // this warp's 16 rows
       const int live = at.end - key0;                              // how many of them are rows of the sequence
       if (live > 0) {
         const uint32_t ks = smem_addr(ring + st * C::STAGE), vs = ks + C::TILE;
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(288, 1)
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[nb][e] = s2[nb][e] = 0.f;
-          const int row = 16 * wq + (lane & 15);
+          const int row = 16 * warp + (lane & 15);
           const uint32_t base = ks + (row >> 3) * C::GROUP + (row & 7) * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(288, 1)
           keep_lo = (r0 < live ? 0xffffu : 0u) | (r0 + 1 < live ? 0xffff0000u : 0u);
           keep_hi = (r0 + 8 < live ? 0xffffu : 0u) | (r0 + 9 < live ? 0xffff0000u : 0u);
         }
-        const int row = 16 * wq + (lane & 7) + 8 * (lane >> 4);
+        const int row = 16 * warp + (lane & 7) + 8 * (lane >> 4);
         const uint32_t base = vs + (row >> 3) * C::GROUP + (row & 7) * 128;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
@@ -530,71 +529,106 @@ __global__ void __launch_bounds__(288, 1)
       if (lane == 0) mbar_arrive(&empty[st]);
     }
 
-    // ---- the eight warps' parts of the unit, through shared memory
+    // ---- the four warps' parts of the unit, through shared memory: warps 2 and
+    // 3 hand theirs to warps 0 and 1 as they hold them, which lay the sums out
+    // by rows for all four to finish
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
           lr[nb][e] += __shfl_xor_sync(0xffffffffu, lr[nb][e], o);
         }
-        const int r = 8 * nb + r0 + e;
+    if (warp >= 2) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+          reinterpret_cast<float4*>(ws)[(mt * NB + nb) * 32 + lane] =
+              make_float4(oacc[mt][nb][0], oacc[mt][nb][1], oacc[mt][nb][2], oacc[mt][nb][3]);
         if (lane < 4) {
-          ws[r] = m[nb][e];
-          ws[C::ROWS + r] = l[nb][e];
-          ws[2 * C::ROWS + r] = lr[nb][e];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float* x = ws + C::ROWS * D + 3 * (8 * nb + r0 + e);
+            x[0] = m[nb][e], x[1] = l[nb][e], x[2] = lr[nb][e];
+          }
+        }
+      }
+    }
+    named_sync(1, 32 * C::WARPS);
+    if (warp < 2) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float f[2], g[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float* x = ws + C::ROWS * D + 3 * (8 * nb + r0 + e);
+          const float mo = x[0], mn = fmaxf(m[nb][e], mo), base = mn == -INFINITY ? 0.f : mn;
+          f[e] = ex2(m[nb][e] - base);
+          g[e] = ex2(mo - base);
+          m[nb][e] = mn;
+          l[nb][e] = f[e] * l[nb][e] + g[e] * x[1];
+          lr[nb][e] = f[e] * lr[nb][e] + g[e] * x[2];
         }
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
-          float* dst = ws + 3 * C::ROWS + r * C::OSTR + 16 * mt + (lane >> 2);
-          dst[0] = oacc[mt][nb][e];
-          dst[8] = oacc[mt][nb][e + 2];
+          const float4 x = reinterpret_cast<const float4*>(ws)[(mt * NB + nb) * 32 + lane];
+          oacc[mt][nb][0] = f[0] * oacc[mt][nb][0] + g[0] * x.x;
+          oacc[mt][nb][1] = f[1] * oacc[mt][nb][1] + g[1] * x.y;
+          oacc[mt][nb][2] = f[0] * oacc[mt][nb][2] + g[0] * x.z;
+          oacc[mt][nb][3] = f[1] * oacc[mt][nb][3] + g[1] * x.w;
         }
       }
-    named_sync(1, 256);
-    if (p.n_pre && !waited) {  // the shared rows' parts
-      pdl_wait();
-      waited = true;
+      __syncwarp();  // every lane has read the other warp's part
+      // m[ROWS] l[ROWS] lr[ROWS] O[ROWS][OSTR]
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nb + r0 + e;
+          if (lane < 4) {
+            ws[r] = m[nb][e];
+            ws[C::ROWS + r] = l[nb][e];
+            ws[2 * C::ROWS + r] = lr[nb][e];
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            float* dst = ws + 3 * C::ROWS + r * C::OSTR + 16 * mt + (lane >> 2);
+            dst[0] = oacc[mt][nb][e];
+            dst[8] = oacc[mt][nb][e + 2];
+          }
+        }
     }
+    named_sync(1, 32 * C::WARPS);
     const bool begins = at.tile == 0, ends = at.tile + n == at.tiles;
     for (int r = warp; r < p.G; r += C::WARPS) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, scratch[w * C::SCRATCH + r]);
-      float lt = 0.f, lrt = 0.f, acc[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
-      if (mm != -INFINITY) {
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float* x = scratch + w * C::SCRATCH;
-          const float f = ex2(x[r] - mm);
-          lt += f * x[C::ROWS + r];
-          lrt += f * x[2 * C::ROWS + r];
-          float ov[VEC];
-          load_vec<VEC>(x + 3 * C::ROWS + r * C::OSTR + VEC * lane, ov);
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) acc[v] += f * ov[v];
-        }
-      }
+      const float *x0 = scratch + r, *x1 = x0 + C::SCRATCH;
+      const float mn = fmaxf(x0[0], x1[0]), base = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(x0[0] - base), g = ex2(x1[0] - base);
+      const float lt = f * x0[C::ROWS] + g * x1[C::ROWS], lrt = f * x0[2 * C::ROWS] + g * x1[2 * C::ROWS];
       // O is normalised by the sum of the weights as rounded for the product,
       // the logarithm is that of the fp32 sum
-      const float inv = lrt > 0.f ? 1.f / lrt : 0.f;
+      const float inv = lrt == 0.f ? 0.f : 1.f / lrt;
+      float u[VEC], v[VEC];
+      load_vec<VEC>(scratch + 3 * C::ROWS + r * C::OSTR + VEC * lane, u);
+      load_vec<VEC>(scratch + C::SCRATCH + 3 * C::ROWS + r * C::OSTR + VEC * lane, v);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[v] *= inv;
-      const float l2 = lt > 0.f ? mm + __log2f(lt) : -INFINITY;
-      if (begins && ends) {
+      for (int i = 0; i < VEC; ++i) u[i] = (f * u[i] + g * v[i]) * inv;
+      if (begins && ends && !p.n_pre) {
         RowSum<VEC> sum;
-        sum.add(l2, acc);
-        const size_t row = q_row + r;
-        add_shared<VEC, NB == 1 ? 8 : 4>(p, row, D, lane, 0, 1, sum);
-        store_row<VEC, BF16>(p, row, D, lane, sum);
+        sum.m = mn;
+        sum.w = 1.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum.o[i] = u[i];
+        store_row<VEC, BF16>(p, q_row + r, D, lane, sum);
+        if (lane == 0) p.lse[q_row + r] = lt == 0.f ? -INFINITY : (mn + __log2f(lt)) * 0.69314718055994531f;
       } else {
         const size_t slot = (size_t)(2 * c + (begins ? 1 : 0)) * p.G + r;
-        store_vec<VEC>(p.o_part + slot * D + VEC * lane, acc);
-        if (lane == 0) p.lse_part[slot] = l2;
+        const bool whole = begins && ends;
+        store_vec<VEC>((whole ? p.own_o + (q_row + r) * D : p.o_part + slot * D) + VEC * lane, u);
+        if (lane == 0) (whole ? p.own_lse[q_row + r] : p.lse_part[slot]) = lt == 0.f ? -INFINITY : mn + __log2f(lt);
       }
     }
     if (begins && !ends) {
@@ -603,57 +637,74 @@ __global__ void __launch_bounds__(288, 1)
       const long long x = t1 + (at.tiles - at.tile - n) - 1;
       cut = PagedCut{at.b, at.kvh, (int)quot((x + 1) * runs - 1, total), 0};
     }
-    named_sync(1, 256);  // the scratch is read before the next unit writes it
+    if (p.n_pre && begins && threadIdx.x == 0) p.unit_cut[(size_t)at.b * p.Hkv + at.kvh] = ends ? -1 : c;
+    named_sync(1, 32 * C::WARPS);  // the scratch is read before the next unit writes it
     left -= n + kUnitCost;
     if (left > 0) at.next_unit(p, C::KT);
   }
   if (threadIdx.x == 0) p.cuts[c] = cut;
-  if (p.n_pre && !waited) pdl_wait();
+  if (p.n_pre) pdl_wait();
 }
 
 // The units that a boundary between CTAs cut: block (c, r) joins the parts of
-// query row r of the unit that CTA c began and did not finish, if any, with
-// the shared rows' parts.  Four warps take the parts in turn.
+// query row r of the unit that CTA c began and did not finish, if any.  Four
+// warps take a quarter of the parts each.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   constexpr int VEC = D / 32;
   __shared__ __align__(16) float s_o[4][D];
-  __shared__ float s_m[4], s_w[4];
+  __shared__ float s_l[4];
   pdl_wait();
   pdl_launch();
   const PagedCut cut = p.cuts[blockIdx.x];
   if (cut.b < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-  const size_t row = (size_t)cut.b * p.Hq + cut.kvh * p.G + r;
-  const int c0 = blockIdx.x, own = cut.last - c0 + 1;
+  const int c0 = blockIdx.x, own = cut.last - c0 + 1, per = (own + 3) / 4, s0 = min(warp * per, own);
+  auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
   RowSum<VEC> sum;
-#pragma unroll 4
-  for (int s = warp; s < own; s += 4) {
-    const size_t slot = (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r;
-    float x[VEC];
-    load_vec<VEC>(p.o_part + slot * D + VEC * lane, x);
-    sum.add(p.lse_part[slot], x);
-  }
-  add_shared<VEC, 8>(p, row, D, lane, warp, 4, sum);
+  add_parts<VEC>(
+      sum, min(per, own - s0), lane, [&](int s) { return p.lse_part[slot(s0 + s)]; },
+      [&](int s) { return p.o_part + slot(s0 + s) * D; });
+  const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sum.o[i] *= inv;
   store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
-  if (lane == 0) s_m[warp] = sum.m, s_w[warp] = sum.w;
+  if (lane == 0) s_l[warp] = sum.w == 0.f ? -INFINITY : sum.m + __log2f(sum.w);
   __syncthreads();
   if (warp) return;
   RowSum<VEC> all;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) all.m = fmaxf(all.m, s_m[w]);
-  if (all.m != -INFINITY) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = ex2(s_m[w] - all.m);
-      all.w += f * s_w[w];
-      float x[VEC];
-      load_vec<VEC>(&s_o[w][VEC * lane], x);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) all.o[v] += f * x[v];
-    }
-  }
-  store_row<VEC, BF16>(p, row, D, lane, all);
+  add_parts<VEC>(all, 4, lane, [&](int s) { return s_l[s]; }, [&](int s) { return s_o[s]; });
+  store_row<VEC, BF16>(p, (size_t)cut.b * p.Hq + cut.kvh * p.G + r, D, lane, all);
+}
+
+// Every row's shared rows' parts and its own, whole or cut: a warp per row.
+// Bound: the n_pre + 1 fp32 parts of every row read once, from L2 mostly.
+// (Joining inside paged_kernel put these loads' latency into every unit's
+// chain: 5 us a unit with 9 parts.)
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+  constexpr int VEC = D / 32;
+  pdl_wait();
+  pdl_launch();
+  const int lane = threadIdx.x & 31;
+  const size_t rows = (size_t)p.B * p.Hq, row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int b = (int)(row / p.Hq), h = (int)(row % p.Hq), kvh = h / p.G, r = h - kvh * p.G;
+  const int c0 = p.unit_cut[(size_t)b * p.Hkv + kvh];
+  const int own = c0 < 0 ? 1 : p.cuts[c0].last - c0 + 1;
+  auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
+  RowSum<VEC> sum;
+  add_parts<VEC>(
+      sum, p.n_pre + own, lane,
+      [&](int s) {
+        return s < p.n_pre ? p.pre_lse[s * rows + row] : c0 < 0 ? p.own_lse[row] : p.lse_part[slot(s - p.n_pre)];
+      },
+      [&](int s) {
+        return s < p.n_pre ? p.pre_o + (s * rows + row) * D
+               : c0 < 0    ? p.own_o + row * D
+                           : p.o_part + slot(s - p.n_pre) * D;
+      });
+  store_row<VEC, BF16>(p, row, D, lane, sum);
 }
 
 }  // namespace fa

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(768, 1)
       const float m = t ? m_row1 : m_row0;
       const float l = sum_buf[((2 * t + 0) * 2 + 0) * 128 + r] + sum_buf[((2 * t + 1) * 2 + 0) * 128 + r];
       const float lr = sum_buf[((2 * t + 0) * 2 + 1) * 128 + r] + sum_buf[((2 * t + 1) * 2 + 1) * 128 + r];
-      const float inv = lr > 0.f ? 1.f / lr : 0.f;
+      const float inv = lr == 0.f ? 0.f : 1.f / lr;
       const int b = seq_of_row(t, r);
       const size_t row = (size_t)split * p.B * p.Hq + (size_t)max(b, 0) * p.Hq + kvh * p.G + r % p.G;
       float4* dst = reinterpret_cast<float4*>(p.pre_o + row * D);
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(768, 1)
                                          __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
         }
       }
-      if (b >= 0) p.pre_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
+      if (b >= 0) p.pre_lse[row] = l == 0.f ? -INFINITY : m + __log2f(l);
     }
   }
 
