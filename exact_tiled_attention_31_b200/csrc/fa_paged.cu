@@ -103,8 +103,12 @@ fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
 bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0; }
 
 // ---------------------------------------------------------------- paged decode
-constexpr int kPagedCtas = 3;  // of paged_kernel on an SM, at most
-int paged_grid() { return kPagedCtas * sm_count(); }
+constexpr int kPagedCtas = 2;  // of paged_kernel on an SM
+// Runs that a call can have: several waves of them (PagedRuns).
+int paged_max_runs() { return kPagedCtas * sm_count() * fa::PagedRuns::kMaxWaves; }
+// A call hands out runs (one more small launch, about 1 us) where its sequences
+// may hold this many tiles a CTA: below, the lag of the slower SMs is not more.
+constexpr long long kClaimTiles = 24;
 
 // Ranges the shared rows are cut into: units = KV heads x query pairs CTAs run
 // one range each.  The cost of n ranges is waves x (tiles of the longest range
@@ -122,27 +126,29 @@ int prefix_splits(long long units, int P) {
 }
 
 struct PagedWs {
-  size_t cuts, lse_part, o_part, pre_lse, pre_o, own_lse, own_o, unit_cut, total;
+  size_t next_run, cuts, lse_part, o_part, pre_lse, pre_o, own_lse, own_o, total;
   int n_pre, n_pairs, per_tile;
 };
 
 PagedWs paged_layout(int B, int Hq, int Hkv, int P, int D) {
   const int G = Hq / Hkv;
-  const size_t parts = (size_t)2 * paged_grid() * G;
+  const int runs = paged_max_runs();
+  const size_t parts = (size_t)2 * runs * G;
   PagedWs w;
   w.per_tile = 128 / G;
   w.n_pairs = (int)(((long long)B + 2 * w.per_tile - 1) / (2 * w.per_tile));
   w.n_pre = P > 0 ? prefix_splits((long long)Hkv * w.n_pairs, P) : 0;
   const size_t pre = (size_t)w.n_pre * B * Hq, own = w.n_pre ? (size_t)B * Hq : 0;
-  w.cuts = 0;
-  w.lse_part = up256(paged_grid() * sizeof(fa::PagedCut));
+  w.next_run = 0;
+  w.cuts = 256;
+  // cuts of all units behind shared rows, else of the runs or units, whichever are fewer
+  w.lse_part = w.cuts + up256((w.n_pre ? std::max((size_t)B * Hkv, (size_t)runs) : (size_t)runs) * sizeof(fa::PagedCut));
   w.o_part = w.lse_part + up256(parts * 4);
   w.pre_lse = w.o_part + up256(parts * D * 4);
   w.pre_o = w.pre_lse + up256(pre * 4);
   w.own_lse = w.pre_o + up256(pre * D * 4);
   w.own_o = w.own_lse + up256(own * 4);
-  w.unit_cut = w.own_o + up256(own * D * 4);
-  w.total = w.unit_cut + up256(w.n_pre ? (size_t)B * Hkv * 4 : 0);
+  w.total = w.own_o + up256(own * D * 4);
   return w;
 }
 
@@ -172,6 +178,13 @@ bool map_queries(CUtensorMap* m, const void* q, int B, int Hkv, int G, int D, bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tiles of the longest sequence that the table can hold, and whether a call is
+// to hand out runs.
+long long paged_tiles(const fa::PagedParams& p) { return std::max(1, (p.map.max_len - p.start + 63) / 64); }
+bool hands_out(const fa::PagedParams& p, long long tiles) {
+  return (long long)p.B * p.Hkv * tiles >= kClaimTiles * kPagedCtas * sm_count();
+}
+
 template <int D, bool BF16, int NB>
 fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_t st) {
   using C = fa::PagedCfg<D, NB>;
@@ -180,16 +193,29 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
   if (!map_pages(&mk, pg.k, pg, D, BF16, box) || !map_pages(&mv, pg.v, pg, D, BF16, box)) return FA_ERR_CUDA;
   if (set_smem<fa::paged_kernel<D, BF16, NB>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
   fa::PagedParams a = p;
-  const long long tiles = std::max(1, (p.map.max_len - p.start + C::KT - 1) / C::KT);  // of the longest sequence
-  static_assert(C::CTAS <= kPagedCtas, "workspace for every CTA");
-  a.grid = (int)std::min<long long>((long long)C::CTAS * sm_count(), (long long)p.B * p.Hkv * tiles);
+  const long long tiles = paged_tiles(p);
+  static_assert(C::CTAS == kPagedCtas && C::KT == 64, "workspace for every run");
+  const long long units = (long long)p.B * p.Hkv, ctas = (long long)C::CTAS * sm_count();
+  a.grid = (int)std::min(ctas, units * tiles);
+  const bool claim = hands_out(p, tiles);
+  a.max_runs = claim ? a.grid * fa::PagedRuns::kMaxWaves : a.grid;
+  a.by_unit = p.n_pre || units <= a.max_runs;
+  if (!claim) a.next_run = nullptr;
+  // (behind shared rows the count was zeroed before them)
+  if (claim && !p.n_pre) {
+    const fa_status s = launch_after(fa::paged_zero_kernel, dim3(1), 32, 0, st, a.next_run);
+    if (s != FA_OK) return s;
+  }
   const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
   if (s != FA_OK) return s;
   if (p.n_pre)
     return launch_after(fa::paged_join_kernel<D, BF16>, dim3((unsigned)(((long long)p.B * p.Hq + 7) / 8)), 256, 0, st, a);
   // units that are never cut: of one tile, or all of them short and on an SM of their own
-  if (tiles == 1 || (tiles <= fa::kWholeTiles && (long long)p.B * p.Hkv <= a.grid)) return FA_OK;
-  return launch_after(fa::paged_merge_kernel<D, BF16>, dim3(a.grid, p.G), 128, 0, st, a);
+  if (tiles == 1 || (tiles <= fa::kWholeTiles && units <= a.grid)) return FA_OK;
+  // a block a row where that is few blocks: long units come in many parts
+  const long long cuts = a.by_unit ? units : a.max_runs;
+  const dim3 grid((unsigned)cuts, cuts * p.G <= 8LL * sm_count() ? p.G : 1);
+  return launch_after(fa::paged_merge_kernel<D, BF16>, grid, 256, 0, st, a);
 }
 
 template <int D, bool BF16>
@@ -210,6 +236,10 @@ template <int D, bool BF16>
 fa_status run_paged(const fa::PagedParams& p, const fa::PrefixParams& pre, const void* q, const fa_pages& pg,
                     cudaStream_t st) {
   if (p.n_pre) {
+    if (hands_out(p, paged_tiles(p))) {
+      const fa_status s = launch_after(fa::paged_zero_kernel, dim3(1), 32, 0, st, p.next_run);
+      if (s != FA_OK) return s;
+    }
     const fa_status s = launch_prefix<D, BF16>(pre, q, pg, st);
     if (s != FA_OK) return s;
   }
@@ -243,13 +273,13 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   p.o_part = reinterpret_cast<float*>(ws + w.o_part);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
   p.cuts = reinterpret_cast<fa::PagedCut*>(ws + w.cuts);
+  p.next_run = reinterpret_cast<int*>(ws + w.next_run);
   p.o = o;
   p.lse = lse;
   p.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
   p.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
   p.own_o = reinterpret_cast<float*>(ws + w.own_o);
   p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
-  p.unit_cut = reinterpret_cast<int*>(ws + w.unit_cut);
   p.n_pre = w.n_pre, p.start = prefix_len;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;

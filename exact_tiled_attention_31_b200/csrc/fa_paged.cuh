@@ -12,11 +12,11 @@
 //
 // Bound: HBM, 4 D bytes a row and KV head, read once.  So the work is dealt
 // out by rows: the tiles of all (sequence, KV head) units, in order, are cut
-// into contiguous runs of equal cost, one per CTA, from the lengths on the
-// device: a ragged batch keeps every SM streaming to the end, whatever its
-// lengths.  A unit that one run covers whole is finished there; the units cut
-// by a boundary (at most one begins in a CTA) leave normalised fp32 parts that
-// paged_merge_kernel joins.
+// into contiguous runs (PagedRuns) from the lengths on the device: a ragged
+// batch keeps every SM streaming to the end, whatever its lengths.  A unit that
+// one run covers whole is finished there; the units cut by a boundary (at most
+// one begins in a run) leave normalised fp32 parts that paged_merge_kernel
+// joins.
 //
 // A CTA has one producer warp, which fills a ring of stages (a tile's K and V
 // rows) by TMA, a box per page, and runs ahead of the consumers over unit
@@ -41,19 +41,32 @@ struct PagedMap {       // how rows of a sequence are found
   int n_pages, page_shift, max_len;  // max_len: rows the table holds
 };
 
-// What CTA c left behind: the unit it began and did not finish, or bh = -1.
+// A cut unit: its first and last run.
 struct PagedCut {
-  int b, kvh, last;  // the unit and the CTA that ends it; b = -1: none
-  int pad;
+  int b, kvh;         // the unit; b = -1: none
+  int first, last;
+};
+
+// What the producer tells the consumers of a segment: the tiles that a run has
+// of one unit.
+struct PagedSeg {
+  int n, key0, end, q_row;  // tiles (0: no more segments), first row, the sequence's length, first query row
+  int begins, ends;         // whether they are the unit's first, last
+  int run, pad;
 };
 
 struct PagedParams {
   const uint16_t* q;     // [B, Hq, D]
   const int* seq_lens;   // [B]
   PagedMap map;
-  float* o_part;         // [2 * grid, G, D] normalised parts: 2c for the unit CTA c goes on with, 2c + 1 begins
-  float* lse_part;       // [2 * grid, G] log2 of the sums
-  PagedCut* cuts;        // [grid]
+  float* o_part;         // [2 * max_runs, G, D] normalised parts: 2c for the unit run c goes on with, 2c + 1 begins
+  float* lse_part;       // [2 * max_runs, G] log2 of the sums
+  // What is cut, by run (the unit that it began and did not finish) where
+  // by_unit is 0, else by unit (the run that begins it): whichever are fewer
+  // (behind shared rows always by unit, for paged_join_kernel).
+  PagedCut* cuts;
+  int by_unit;
+  int* next_run;         // zeroed, counts the short runs taken; null: CTA c has run c alone
   void* o;               // [B, Hq, D]
   float* lse;            // [B, Hq]
   // With shared rows [0, start) in front (n_pre > 0) nothing is finished here:
@@ -62,9 +75,8 @@ struct PagedParams {
   const float* pre_lse;  // [n_pre, B * Hq]
   float* own_o;          // [B * Hq, D] parts of units that are not cut
   float* own_lse;        // [B * Hq]
-  int* unit_cut;         // [B * Hkv] the CTA that begins a cut unit, or -1
   int n_pre, start;
-  int B, Hq, Hkv, G, grid;
+  int B, Hq, Hkv, G, grid, max_runs;
   float scale_log2;
 };
 
@@ -75,15 +87,16 @@ struct PagedCfg {
   static constexpr int GROUP = D * 16;                 // 8 rows: D / 64 swizzle atoms of 1 KB
   static constexpr int TILE = KT * D * 2;              // K or V
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int STAGES = (D == 128 ? 3 : 6) - (NB == 2 && D == 128);
+  static constexpr int STAGES = (D == 128 ? 3 : 6) - (NB == 2);  // 64 to 96 KB in flight per CTA
   static constexpr int CTAS = 2;  // per SM
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int OSTR = D + 4;                   // fp32 row stride of the scratch: conflict-free
   static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats of one warp's part
-  static constexpr uint32_t SMEM = STAGES * STAGE + 2 * SCRATCH * 4 + 1024;
+  static constexpr int QTILE = ROWS * D * 2;           // queries of a segment
+  static constexpr uint32_t SMEM = STAGES * (STAGE + QTILE) + 2 * SCRATCH * 4 + 1024;
   // with the barriers and the run's place, and 1 KB that the system takes
-  static_assert(CTAS * (SMEM + 256 + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(CTAS * (SMEM + 1280 + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
@@ -120,16 +133,38 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+// a plain copy of `bytes` (a multiple of 16) into shared memory
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+// named barrier over `count` threads: whether `ok` holds in all of them
+__device__ __forceinline__ bool named_and(uint32_t id, uint32_t count, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ uint32_t movm_trans(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
-// Page of box `first row` of sequence b, or n_pages (out of the pool: TMA
-// fills zeros) with an argument error where the table names none.
-__device__ __forceinline__ int page_of(const PagedMap& m, const int* row, int first) {
-  const int id = row[first >> m.page_shift];
+// The page that a table entry names, or n_pages (out of the pool: TMA fills
+// zeros) with an argument error where it names none.
+__device__ __forceinline__ int page_ok(const PagedMap& m, int id) {
   if (id >= 0 && id < m.n_pages) return id;
   record_error(DEV_ERR_ARG, PAGED_SITE_PAGE);
   return m.n_pages;
@@ -171,6 +206,12 @@ __device__ __forceinline__ void add_parts(RowSum<VEC>& sum, int n, int lane, L&&
   for (int s0 = 0; s0 < n; s0 += 32) {
     const int k = min(32, n - s0);
     const float l = lane < k ? l2(s0 + lane) : -INFINITY;
+    float x[FLY][VEC];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) load_vec<VEC>(o(s0 + min(j + f, k - 1)) + VEC * lane, x[f]);
+    };
+    fetch(0);
     float mn = l;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
@@ -185,9 +226,7 @@ __device__ __forceinline__ void add_parts(RowSum<VEC>& sum, int n, int lane, L&&
 #pragma unroll
     for (int i = 0; i < VEC; ++i) sum.o[i] *= a;
     for (int j = 0; j < k; j += FLY) {
-      float x[FLY][VEC];
-#pragma unroll
-      for (int f = 0; f < FLY; ++f) load_vec<VEC>(o(s0 + min(j + f, k - 1)) + VEC * lane, x[f]);
+      if (j > 0) fetch(j);
 #pragma unroll
       for (int f = 0; f < FLY; ++f) {
         const float wf = j + f < k ? __shfl_sync(0xffffffffu, w, j + f) : 0.f;
@@ -225,6 +264,55 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
+// The cost Hkv * sum_b (tiles(b) + kUnitCost) of a call, cut into runs.  CTAs do
+// not stream equally fast: on B200 whole groups of SMs get up to 8 % less than
+// the mean, others 8 % more (32 x 8 caches of 8192 rows in equal runs: the
+// first SM done after 135 us, the last after 160, 149 on average).  So where
+// there is enough to do, each of S equal stretches of the list is one long run
+// and some short ones, in order; CTA c begins with the long run of stretch c,
+// and then whoever comes first takes the next of the short ones, all second
+// ones of the stretches before the third ones.  Which CTA takes a run does not
+// change the runs, so results do not depend on it.  (With the short runs at the
+// end of the list its last units came in up to a hundred parts, and joining
+// them cost more than the balance gained.)
+struct PagedRuns {
+  long long total;
+  int S, runs, waves;  // CTAs; runs in all; runs of a stretch (1: `runs` equal ones)
+  static constexpr int kMaxWaves = 5;
+  // where in a stretch a run begins, in 256ths: 192 32 20 12, or 176 40 20 12 8
+  static __device__ __forceinline__ int share(int waves, int w) {
+    constexpr uint64_t kFour = 192ull << 8 | 224ull << 16 | 244ull << 24;
+    constexpr uint64_t kFive = 176ull << 8 | 216ull << 16 | 236ull << 24 | 248ull << 32;
+    return w == waves ? 256 : (int)((waves == 4 ? kFour : kFive) >> (8 * w)) & 255;
+  }
+  __device__ __forceinline__ PagedRuns(long long total, long long units, int grid, bool claim)
+      : total(total), S(grid), runs((int)min((long long)grid, max(units, total / kMinRun))), waves(1) {
+    // the shortest run is a tile (a part each) in four, two in five
+    const long long per = quot(total, grid);
+    if (claim && per >= 24 && per < (1LL << 24)) {
+      waves = per < 64 ? 4 : 5;
+      runs = waves * S;
+    }
+  }
+  // place in the list of the i-th run to be taken
+  __device__ __forceinline__ int place(int i) const { return waves == 1 ? i : (i % S) * waves + i / S; }
+  // cost in front of run c (by place)
+  __device__ __forceinline__ long long begin(int c) const {
+    if (waves == 1) return quot(c * total, runs);
+    const int g = c / waves, w = c - g * waves;
+    return (g * 256LL + (w ? share(waves, w) : 0)) * total / (256LL * S);
+  }
+  // the run that cost x lies in: the largest c with begin(c) <= x
+  __device__ __forceinline__ int of(long long x) const {
+    if (waves == 1) return (int)quot((x + 1) * runs - 1, total);
+    const long long n = ((x + 1) * 256 * S - 1) / total;
+    const int g = (int)(n >> 8), in = (int)(n & 255);
+    int w = waves - 1;
+    while (w > 0 && share(waves, w) > in) --w;
+    return g * waves + w;
+  }
+};
+
 // A place in the list of tiles: (sequence, KV head) units in order, each of
 // its sequence's tiles.  A sequence without rows of its own still has one
 // (empty) tile, so that its outputs are written.
@@ -251,12 +339,14 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
   using C = PagedCfg<D, NB>;
   constexpr int VEC = D / 32;
   extern __shared__ uint8_t dsm_raw[];
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], seg_full[C::STAGES];
+  __shared__ __align__(16) PagedSeg segs[C::STAGES];
+  constexpr int FIND = 32 * C::WARPS;  // threads that sum the lengths, a chunk of sequences each
   __shared__ int warp_max[C::WARPS];
-  __shared__ long long warp_sum[C::WARPS], s_first;  // cost before the first sequence of this run
-  __shared__ int s_b;
+  __shared__ long long warp_sum[C::WARPS], sums[FIND];  // cost of the sequences before a chunk
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
-  float* scratch = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
+  uint8_t* queries = ring + C::STAGES * C::STAGE;
+  float* scratch = reinterpret_cast<float*>(queries + C::STAGES * C::QTILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
 
@@ -264,24 +354,30 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], C::WARPS);
+      mbar_init(&seg_full[s], 1);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    s_b = 0;
-    s_first = 0;
+  }
+  // On their way into L2 while the kernel ahead ends: the lengths, queries and
+  // first lines of the table (only cached here, read after the wait).
+  {
+    const long long i = (long long)c * C::THREADS + threadIdx.x;
+    if (i * 64 < (long long)p.B * p.Hq * D) prefetch_l2(p.q + i * 64);
+    if (i * 32 < p.B) prefetch_l2(p.seq_lens + i * 32);
+    if (i < p.B) prefetch_l2(p.map.table + i * p.map.table_stride + (p.start >> p.map.page_shift));
   }
   // Behind prefix_kernel (which has itself waited for all before it) this kernel
   // runs ahead: it reads nothing of that one's, and only waits for its end.
   if (!p.n_pre) pdl_wait();
   pdl_launch();
 
-  // ---- this CTA's run [t0, t1) of the cost Hkv * sum_b (tiles(b) + kUnitCost)
+  // ---- the cost of the call
   auto cost_of = [&](int b) {
     const int end = min(max(p.seq_lens[b], 0), p.map.max_len);
     return max(1, (end - p.start + C::KT - 1) / C::KT) + kUnitCost;
   };
-  constexpr int FIND = 32 * C::WARPS;  // threads that look for the run
   const int chunk = (p.B + FIND - 1) / FIND;
   const int b_lo = (int)min((long long)threadIdx.x * chunk, (long long)p.B);
   const int b_hi = threadIdx.x < FIND ? min(b_lo + chunk, p.B) : b_lo;
@@ -312,88 +408,152 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     most = max(most, warp_max[w]);
   }
   total *= p.Hkv;
-  // Tile k of a unit sits kUnitCost + k behind the unit's start.  At most as
-  // many runs as there is cost, so that no run inside a unit is without a tile.
   const long long units = (long long)p.B * p.Hkv;
-  const int runs = (int)min((long long)p.grid, max(units, total / kMinRun));
-  const long long t0 = c < runs ? quot(c * total, runs) : 0,
-                  t1 = c < runs ? quot((c + 1) * total, runs) : 0;
-  if (threadIdx.x < FIND && t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
-    int b = b_lo;
-    for (; b < b_hi - 1; ++b) {
-      const int n = cost_of(b);
-      if (t0 < (before + n) * p.Hkv) break;
-      before += n;
-    }
-    s_b = b;
-    s_first = before * p.Hkv;
-  }
+  const PagedRuns runs(total, units, p.grid, p.next_run != nullptr);
+  const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA: a unit each
+  if (threadIdx.x < FIND) sums[threadIdx.x] = before;
   __syncthreads();
-  PagedWalk at;
-  long long left;  // cost of what is left of the run, from tile at.tile on
-  if (units <= p.grid && most <= kWholeTiles + kUnitCost) {  // the same in every CTA: a unit each
-    at.b = min(c / p.Hkv, p.B - 1);
-    at.load(p, C::KT);
-    at.kvh = c % p.Hkv;
-    at.tile = 0;
-    left = c < units ? at.tiles : 0;
-  } else {
-    at.b = s_b;
-    at.load(p, C::KT);
-    const int cost = at.tiles + kUnitCost;
-    at.kvh = (int)quot(t0 - s_first, cost);
-    const int off = (int)(t0 - s_first - (long long)at.kvh * cost);  // into the unit
-    at.tile = max(0, off - kUnitCost);
-    left = t1 - t0 - max(0, kUnitCost - off);
-  }
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- producer
+    // The first tile of run c and the cost of what the run holds from it on.
+    // Tile k of a unit sits kUnitCost + k behind the unit's start; there are at
+    // most as many runs as there is cost, so no run inside a unit is without a
+    // tile.
+    auto enter = [&](int c, PagedWalk& at, long long& t1) -> long long {
+      const long long t0 = runs.begin(c);
+      t1 = runs.begin(c + 1);
+      // the last chunk that begins at or before t0 (those behind the last
+      // sequence begin at the total)
+      int lo = 0;
+#pragma unroll
+      for (int k = 0; k < FIND; k += 32) lo += __popc(__ballot_sync(0xffffffffu, sums[k + lane] * p.Hkv <= t0));
+      long long first = sums[lo - 1];
+      at.b = min((lo - 1) * chunk, p.B - 1);
+      for (;;) {
+        const int n = cost_of(at.b);
+        if (t0 < (first + n) * p.Hkv || at.b == p.B - 1) break;
+        first += n;
+        ++at.b;
+      }
+      first *= p.Hkv;
+      at.load(p, C::KT);
+      const int cost = at.tiles + kUnitCost;
+      at.kvh = (int)quot(t0 - first, cost);
+      const int off = (int)(t0 - first - (long long)at.kvh * cost);  // into the unit
+      at.tile = max(0, off - kUnitCost);
+      return t1 - t0 - max(0, kUnitCost - off);
+    };
+    PagedWalk at;
+    int run = c;
+    long long left = 0, t1 = 0;  // cost of what is left of the run, from tile at.tile on; the run's end
+    if (whole) {
+      if (c < units) {
+        at.b = c / p.Hkv;
+        at.load(p, C::KT);
+        at.kvh = c % p.Hkv;
+        at.tile = 0;
+        left = at.tiles;
+      }
+    } else if (c < runs.runs) {
+      run = runs.place(c);
+      left = enter(run, at, t1);
+    }
     const int box = min(C::KT, 1 << p.map.page_shift), boxes = C::KT / box;  // rows per box, boxes per tile
     const int batch = 32 / boxes;                                            // tiles whose pages one load finds
     const int my_box = lane >> 1, my_v = lane & 1;                           // the copy this lane issues: <= 8 of them
-    uint32_t it = 0;
+    uint32_t it = 0, seg = 0;  // tiles, segments so far
     bool ok = true;
-    while (left > 0 && ok) {
-      const int n = (int)min((long long)(at.tiles - at.tile), left);
-      const int* row = p.map.table + at.b * p.map.table_stride;
-      // page of this lane's (tile, box) of the batch from tile k on
-      auto find = [&](int k) {
-        const int i = k + lane / boxes;
-        const int first = p.start + (at.tile + i) * C::KT + (lane % boxes) * box;
-        return i < n && lane < batch * boxes && first < at.end ? page_of(p.map, row, first) : -1;
-      };
-      int ids = find(0);
-      for (int k = 0; k < n && ok; k += batch) {
-        const int ids_next = find(k + batch);
-        for (int i = k; i < min(k + batch, n); ++i, ++it) {
-          const uint32_t st = it % C::STAGES, round = it / C::STAGES;
-          if (round > 0 &&
-              !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (round - 1) & 1, PAGED_SITE_EMPTY))))
-            break;
-          const int key0 = p.start + (at.tile + i) * C::KT;
-          // boxes that hold rows of the sequence; the rest of the stage is left as it is and masked
-          const int live = at.end > key0 ? min(boxes, (at.end - key0 + box - 1) / box) : 0;
-          if (lane == 0) {
-            if (live) mbar_expect_tx(&full[st], live * box * D * 4);
-            else mbar_arrive(&full[st]);
+    // runs that there are not hold no cut
+    if (!p.by_unit)
+      for (int r = c + p.grid * lane; r < p.max_runs; r += 32 * p.grid)
+        if (whole || r >= runs.runs) p.cuts[r].b = -1;
+    // the stage of the next tile, free.  The tiles of the last STAGES - 1
+    // segments and this one are in the ring at most, so a slot for each stage
+    // is enough for what is told of segments.
+    auto take = [&]() {
+      const uint32_t st = it % C::STAGES, round = it / C::STAGES;
+      if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (round - 1) & 1, PAGED_SITE_EMPTY));
+      return st;
+    };
+    for (;;) {
+      PagedCut run_cut{-1, 0, 0, 0};
+      while (left > 0 && ok) {
+        const int n = (int)min((long long)(at.tiles - at.tile), left);
+        const bool begins = at.tile == 0, ends = at.tile + n == at.tiles;
+        const int* row = p.map.table + at.b * p.map.table_stride;
+        // table entry of this lane's (tile, box) of the batch from tile k on
+        auto find = [&](int k) {
+          const int i = k + lane / boxes;
+          const int first = p.start + (at.tile + i) * C::KT + (lane % boxes) * box;
+          return i < n && lane < batch * boxes && first < at.end ? row[first >> p.map.page_shift] : -1;
+        };
+        int ids = find(0);
+        for (int k = 0; k < n && ok; k += batch) {
+          const int ids_next = find(k + batch);
+          for (int i = k; i < min(k + batch, n); ++i, ++it) {
+            const uint32_t st = take();
+            if (!ok) break;
+            const int key0 = p.start + (at.tile + i) * C::KT;
+            if (i == 0 && lane == 0) {
+              const uint32_t sl = seg % C::STAGES;
+              const int q_row = at.b * p.Hq + at.kvh * p.G;
+              segs[sl] = PagedSeg{n, key0, at.end, q_row, begins, ends, run, 0};
+              mbar_expect_tx(&seg_full[sl], p.G * D * 2);
+              bulk_load(queries + sl * C::QTILE, p.q + (size_t)q_row * D, p.G * D * 2, &seg_full[sl]);
+            }
+            // boxes that hold rows of the sequence; the rest of the stage is left as it is and masked
+            const int live = at.end > key0 ? min(boxes, (at.end - key0 + box - 1) / box) : 0;
+            if (lane == 0) {
+              if (live) mbar_expect_tx(&full[st], live * box * D * 4);
+              else mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            const int id = __shfl_sync(0xffffffffu, ids, (i - k) * boxes + min(my_box, boxes - 1));
+            if (my_box < live) {
+              uint8_t* dst = ring + st * C::STAGE + my_v * C::TILE + my_box * box * D * 2;
+              const int first = (key0 + my_box * box) & ((1 << p.map.page_shift) - 1);  // row in its page
+              load_rows(dst, my_v ? &tm_v : &tm_k, &full[st], ((at.kvh << p.map.page_shift) + first) >> 3,
+                        page_ok(p.map, id));
+            }
           }
-          __syncwarp();
-          const int id = __shfl_sync(0xffffffffu, ids, (i - k) * boxes + min(my_box, boxes - 1));
-          if (my_box < live) {
-            uint8_t* dst = ring + st * C::STAGE + my_v * C::TILE + my_box * box * D * 2;
-            const int first = (key0 + my_box * box) & ((1 << p.map.page_shift) - 1);  // row in its page
-            load_rows(dst, my_v ? &tm_v : &tm_k, &full[st], ((at.kvh << p.map.page_shift) + first) >> 3, id);
-          }
+          ids = ids_next;
         }
-        ids = ids_next;
+        ++seg;
+        if (begins) {
+          PagedCut cut{-1, 0, 0, 0};
+          if (!ends) cut = PagedCut{at.b, at.kvh, run, runs.of(t1 + (at.tiles - at.tile - n) - 1)};
+          if (!p.by_unit) run_cut = cut;
+          else if (lane == 0) p.cuts[(size_t)at.b * p.Hkv + at.kvh] = cut;
+        }
+        left -= n + kUnitCost;  // the next unit's own cost too
+        if (left > 0) at.next_unit(p, C::KT);
       }
-      left -= n + kUnitCost;  // the next unit's own cost too
-      if (left > 0) at.next_unit(p, C::KT);
+      if (lane == 0 && !p.by_unit && !whole && c < runs.runs) p.cuts[run] = run_cut;
+      if (!ok || whole || runs.waves == 1) break;
+      int i = 0;
+      if (lane == 0) i = p.grid + atomicAdd(p.next_run, 1);
+      i = __shfl_sync(0xffffffffu, i, 0);
+      if (i >= runs.runs) break;
+      run = runs.place(i);
+      left = enter(run, at, t1);
     }
-    // no copy may still be on its way into shared memory when the CTA ends
+    if (ok) {  // no more
+      take();
+      if (ok) {
+        if (lane == 0) {
+          segs[seg % C::STAGES].n = 0;
+          mbar_arrive(&seg_full[seg % C::STAGES]);
+        }
+        ++seg;
+      }
+    }
+    // no copy may still be on its way into shared memory when the CTA ends: the
+    // newest phase of every barrier
     for (uint32_t f = it > C::STAGES ? it - C::STAGES : 0; f < it; ++f)
       mbar_wait(&full[f % C::STAGES], (f / C::STAGES) & 1, PAGED_SITE_DRAIN);
+    for (uint32_t f = seg > C::STAGES ? seg - C::STAGES : 0; f < seg; ++f)
+      mbar_wait(&seg_full[f % C::STAGES], (f / C::STAGES) & 1, PAGED_SITE_DRAIN);
     __syncwarp();
     if (p.n_pre) pdl_wait();
     return;
@@ -403,18 +563,24 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
   const int r0 = 2 * (lane & 3);  // this lane's query rows 8 nb + r0, + 1; its cache rows lane / 4, + 8
   // one of two parts in the scratch: of warps w and w + 2
   float* ws = scratch + (warp & 1) * C::SCRATCH;
-  uint32_t it = 0;
+  uint32_t it = 0, seg = 0;
   bool ok = true;
-  PagedCut cut{-1, 0, 0, 0};
-  while (left > 0) {
-    const int n = (int)min((long long)(at.tiles - at.tile), left);
-    const size_t q_row = (size_t)at.b * p.Hq + at.kvh * p.G;
+  for (;; ++seg) {
+    const uint32_t sl = seg % C::STAGES;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&seg_full[sl], (seg / C::STAGES) & 1, PAGED_SITE_FULL));
+    // all four warps go on, or none does (this also ends the reads of the
+    // scratch by the segment before)
+    if (!named_and(1, 32 * C::WARPS, ok)) break;
+    const PagedSeg sg = segs[sl];
+    const int n = sg.n;
+    if (n == 0) break;
+    const size_t q_row = sg.q_row;
     // Q^T as the B operand: column lane / 4 of each 8 is a query row
     uint32_t qb[NB][D / 16][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = 8 * nb + (lane >> 2);
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (q_row + r) * D) + (lane & 3);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(queries + sl * C::QTILE + r * D * 2) + (lane & 3);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qb[nb][kk][0] = r < p.G ? q[8 * kk] : 0u;
@@ -436,8 +602,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
       const uint32_t st = it % C::STAGES;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / C::STAGES) & 1, PAGED_SITE_FULL));
       if (!ok) continue;  // error recorded: take no more tiles, but keep to the barriers below
-      const int key0 = p.start + (at.tile + i) * C::KT + 16 * warp;  // this warp's 16 rows
-      const int live = at.end - key0;                              // how many of them are rows of the sequence
+      const int key0 = sg.key0 + i * C::KT + 16 * warp;  // this warp's 16 rows
+      const int live = sg.end - key0;                              // how many of them are rows of the sequence
       if (live > 0) {
         const uint32_t ks = smem_addr(ring + st * C::STAGE), vs = ks + C::TILE;
         // S^T = K Q^T
@@ -602,7 +768,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
         }
     }
     named_sync(1, 32 * C::WARPS);
-    const bool begins = at.tile == 0, ends = at.tile + n == at.tiles;
+    const bool begins = sg.begins, ends = sg.ends;
     for (int r = warp; r < p.G; r += C::WARPS) {
       const float *x0 = scratch + r, *x1 = x0 + C::SCRATCH;
       const float mn = fmaxf(x0[0], x1[0]), base = mn == -INFINITY ? 0.f : mn;
@@ -625,56 +791,69 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
         store_row<VEC, BF16>(p, q_row + r, D, lane, sum);
         if (lane == 0) p.lse[q_row + r] = lt == 0.f ? -INFINITY : (mn + __log2f(lt)) * 0.69314718055994531f;
       } else {
-        const size_t slot = (size_t)(2 * c + (begins ? 1 : 0)) * p.G + r;
+        const size_t slot = (size_t)(2 * sg.run + (begins ? 1 : 0)) * p.G + r;
         const bool whole = begins && ends;
         store_vec<VEC>((whole ? p.own_o + (q_row + r) * D : p.o_part + slot * D) + VEC * lane, u);
         if (lane == 0) (whole ? p.own_lse[q_row + r] : p.lse_part[slot]) = lt == 0.f ? -INFINITY : mn + __log2f(lt);
       }
     }
-    if (begins && !ends) {
-      // the CTA that runs the unit's last tile x: the largest c' with
-      // floor(c' total / runs) <= x
-      const long long x = t1 + (at.tiles - at.tile - n) - 1;
-      cut = PagedCut{at.b, at.kvh, (int)quot((x + 1) * runs - 1, total), 0};
-    }
-    if (p.n_pre && begins && threadIdx.x == 0) p.unit_cut[(size_t)at.b * p.Hkv + at.kvh] = ends ? -1 : c;
-    named_sync(1, 32 * C::WARPS);  // the scratch is read before the next unit writes it
-    left -= n + kUnitCost;
-    if (left > 0) at.next_unit(p, C::KT);
   }
-  if (threadIdx.x == 0) p.cuts[c] = cut;
   if (p.n_pre) pdl_wait();
 }
 
-// The units that a boundary between CTAs cut: block (c, r) joins the parts of
-// query row r of the unit that CTA c began and did not finish, if any.  Four
-// warps take a quarter of the parts each.
+// Before a call that hands out runs: the count of them.
+__global__ void __launch_bounds__(32) paged_zero_kernel(int* next_run) {
+  pdl_launch();  // what follows waits for this kernel, and so for all before it
+  pdl_wait();
+  if (threadIdx.x == 0) *next_run = 0;
+}
+
+// Whether a cut is one (an erring paged_kernel may have left anything).
+__device__ __forceinline__ bool cut_ok(const PagedParams& p, const PagedCut& cut) {
+  return cut.b >= 0 && cut.b < p.B && cut.kvh >= 0 && cut.kvh < p.Hkv && cut.first >= 0 && cut.last > cut.first &&
+         cut.last < p.max_runs;
+}
+
+// The units that a boundary between runs cut: a block joins the parts of the
+// query rows of one of p.cuts, if it is a cut: all of them, or (grid.y = G)
+// one, and then all its warps share the row's parts.  Bound: the latency of three dependent reads.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
-  constexpr int VEC = D / 32;
-  __shared__ __align__(16) float s_o[4][D];
-  __shared__ float s_l[4];
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
+  constexpr int VEC = D / 32, WARPS = 8;
+  __shared__ __align__(16) float s_o[WARPS][D];
+  __shared__ float s_l[WARPS];
   pdl_wait();
   pdl_launch();
   const PagedCut cut = p.cuts[blockIdx.x];
-  if (cut.b < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-  const int c0 = blockIdx.x, own = cut.last - c0 + 1, per = (own + 3) / 4, s0 = min(warp * per, own);
-  auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
-  RowSum<VEC> sum;
-  add_parts<VEC>(
-      sum, min(per, own - s0), lane, [&](int s) { return p.lse_part[slot(s0 + s)]; },
-      [&](int s) { return p.o_part + slot(s0 + s) * D; });
-  const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
+  if (!cut_ok(p, cut)) return;
+  const int c0 = cut.first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = gridDim.y > 1 ? 1 : p.G, r_lo = blockIdx.y;  // this block's rows
+  const int split = max(1, WARPS / rows);                       // warps of a row
+  const int sub = warp % split, own = cut.last - c0 + 1, per = (own + split - 1) / split, s0 = min(sub * per, own);
+  const size_t row0 = (size_t)cut.b * p.Hq + cut.kvh * p.G;
+  for (int r = r_lo + warp / split; r < r_lo + rows; r += WARPS / split) {
+    auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
+    RowSum<VEC> sum;
+    add_parts<VEC>(
+        sum, min(per, own - s0), lane, [&](int s) { return p.lse_part[slot(s0 + s)]; },
+        [&](int s) { return p.o_part + slot(s0 + s) * D; });
+    if (split == 1) {
+      store_row<VEC, BF16>(p, row0 + r, D, lane, sum);
+      continue;
+    }
+    const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) sum.o[i] *= inv;
-  store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
-  if (lane == 0) s_l[warp] = sum.w == 0.f ? -INFINITY : sum.m + __log2f(sum.w);
+    for (int i = 0; i < VEC; ++i) sum.o[i] *= inv;
+    store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
+    if (lane == 0) s_l[warp] = sum.w == 0.f ? -INFINITY : sum.m + __log2f(sum.w);
+  }
+  if (split == 1) return;
   __syncthreads();
-  if (warp) return;
+  if (sub || warp / split >= rows) return;
   RowSum<VEC> all;
-  add_parts<VEC>(all, 4, lane, [&](int s) { return s_l[s]; }, [&](int s) { return s_o[s]; });
-  store_row<VEC, BF16>(p, (size_t)cut.b * p.Hq + cut.kvh * p.G + r, D, lane, all);
+  add_parts<VEC>(all, split, lane, [&](int s) { return s_l[warp + s]; }, [&](int s) { return s_o[warp + s]; });
+  store_row<VEC, BF16>(p, row0 + r_lo + warp / split, D, lane, all);
 }
 
 // Every row's shared rows' parts and its own, whole or cut: a warp per row.
@@ -690,19 +869,20 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   const size_t rows = (size_t)p.B * p.Hq, row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int b = (int)(row / p.Hq), h = (int)(row % p.Hq), kvh = h / p.G, r = h - kvh * p.G;
-  const int c0 = p.unit_cut[(size_t)b * p.Hkv + kvh];
-  const int own = c0 < 0 ? 1 : p.cuts[c0].last - c0 + 1;
+  const PagedCut cut = p.cuts[(size_t)b * p.Hkv + kvh];
+  const bool is_cut = cut_ok(p, cut);
+  const int c0 = cut.first, own = is_cut ? cut.last - c0 + 1 : 1;
   auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
   RowSum<VEC> sum;
   add_parts<VEC>(
       sum, p.n_pre + own, lane,
       [&](int s) {
-        return s < p.n_pre ? p.pre_lse[s * rows + row] : c0 < 0 ? p.own_lse[row] : p.lse_part[slot(s - p.n_pre)];
+        return s < p.n_pre ? p.pre_lse[s * rows + row] : is_cut ? p.lse_part[slot(s - p.n_pre)] : p.own_lse[row];
       },
       [&](int s) {
         return s < p.n_pre ? p.pre_o + (s * rows + row) * D
-               : c0 < 0    ? p.own_o + row * D
-                           : p.o_part + slot(s - p.n_pre) * D;
+               : is_cut    ? p.o_part + slot(s - p.n_pre) * D
+                           : p.own_o + row * D;
       });
   store_row<VEC, BF16>(p, row, D, lane, sum);
 }

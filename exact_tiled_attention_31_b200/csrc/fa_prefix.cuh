@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(768, 1)
       // page of this lane's box of tile j; past the shared rows zeros are filled
       auto find = [&](int j) {
         const int first = (j0 + j) * 128 + my_box * box;
-        return active && j < n_kv && first < p.P ? page_of(p.map, p.map.table, first) : p.map.n_pages;
+        return active && j < n_kv && first < p.P ? page_ok(p.map, p.map.table[first >> p.map.page_shift]) : p.map.n_pages;
       };
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
