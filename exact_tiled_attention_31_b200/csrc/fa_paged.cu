@@ -106,9 +106,6 @@ bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_di
 constexpr int kPagedCtas = 2;  // of paged_kernel on an SM
 // Runs that a call can have: several waves of them (PagedRuns).
 int paged_max_runs() { return kPagedCtas * sm_count() * fa::PagedRuns::kMaxWaves; }
-// A call hands out runs (one more small launch, about 1 us) where its sequences
-// may hold this many tiles a CTA: below, the lag of the slower SMs is not more.
-constexpr long long kClaimTiles = 24;
 
 // Ranges the shared rows are cut into: units = KV heads x query pairs CTAs run
 // one range each.  The cost of n ranges is waves x (tiles of the longest range
@@ -178,11 +175,11 @@ bool map_queries(CUtensorMap* m, const void* q, int B, int Hkv, int G, int D, bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tiles of the longest sequence that the table can hold, and whether a call is
-// to hand out runs.
+// Tiles of the longest sequence that the table can hold, and whether a call may
+// hand out runs (which takes one more small launch, about 1 us).
 long long paged_tiles(const fa::PagedParams& p) { return std::max(1, (p.map.max_len - p.start + 63) / 64); }
 bool hands_out(const fa::PagedParams& p, long long tiles) {
-  return (long long)p.B * p.Hkv * tiles >= kClaimTiles * kPagedCtas * sm_count();
+  return (long long)p.B * p.Hkv * tiles >= fa::kClaimTiles * kPagedCtas * sm_count();
 }
 
 template <int D, bool BF16, int NB>
@@ -212,9 +209,10 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
     return launch_after(fa::paged_join_kernel<D, BF16>, dim3((unsigned)(((long long)p.B * p.Hq + 7) / 8)), 256, 0, st, a);
   // units that are never cut: of one tile, or all of them short and on an SM of their own
   if (tiles == 1 || (tiles <= fa::kWholeTiles && units <= a.grid)) return FA_OK;
-  // a block a row where that is few blocks: long units come in many parts
+  // few rows to a block (and so many warps to a row) as long as the blocks, three
+  // to an SM, run at once
   const long long cuts = a.by_unit ? units : a.max_runs;
-  const dim3 grid((unsigned)cuts, cuts * p.G <= 8LL * sm_count() ? p.G : 1);
+  const dim3 grid((unsigned)cuts, (unsigned)std::max(1LL, std::min<long long>(p.G, 3LL * sm_count() / cuts)));
   return launch_after(fa::paged_merge_kernel<D, BF16>, grid, 256, 0, st, a);
 }
 

@@ -95,11 +95,13 @@ struct PagedCfg {
   static constexpr int SCRATCH = ROWS * (3 + OSTR);    // floats of one warp's part
   static constexpr int QTILE = ROWS * D * 2;           // queries of a segment
   static constexpr uint32_t SMEM = STAGES * (STAGE + QTILE) + 2 * SCRATCH * 4 + 1024;
-  // with the barriers and the run's place, and 1 KB that the system takes
-  static_assert(CTAS * (SMEM + 1280 + 1024) <= 228 * 1024, "shared memory of an SM");
+  // with the static part, and 1 KB a CTA that the system takes
+  static constexpr uint32_t STATIC = 1408;
+  static_assert(CTAS * (SMEM + STATIC + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
+enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413,
+                PAGED_SITE_ROWS = 0x414 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
@@ -258,6 +260,8 @@ constexpr int kUnitCost = 2;
 constexpr int kWholeTiles = 8;
 // Below this cost a run is not worth a CTA and a part.
 constexpr int kMinRun = 4;
+// From this many tiles a CTA on runs are handed out.
+constexpr long long kClaimTiles = 48;
 
 // floor(a / b), b > 0, a >= 0: by 32-bit division where both fit
 __device__ __forceinline__ long long quot(long long a, long long b) {
@@ -278,19 +282,18 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 struct PagedRuns {
   long long total;
   int S, runs, waves;  // CTAs; runs in all; runs of a stretch (1: `runs` equal ones)
-  static constexpr int kMaxWaves = 5;
-  // where in a stretch a run begins, in 256ths: 192 32 20 12, or 176 40 20 12 8
-  static __device__ __forceinline__ int share(int waves, int w) {
-    constexpr uint64_t kFour = 192ull << 8 | 224ull << 16 | 244ull << 24;
-    constexpr uint64_t kFive = 176ull << 8 | 216ull << 16 | 236ull << 24 | 248ull << 32;
-    return w == waves ? 256 : (int)((waves == 4 ? kFour : kFive) >> (8 * w)) & 255;
-  }
+  static constexpr int kMaxWaves = 3;
+  // where in a stretch its runs begin, in 256ths: they are 208, 32 and 16 long
+  static __device__ __forceinline__ int share(int w) { return w == 0 ? 0 : w == 1 ? 208 : 240; }
   __device__ __forceinline__ PagedRuns(long long total, long long units, int grid, bool claim)
       : total(total), S(grid), runs((int)min((long long)grid, max(units, total / kMinRun))), waves(1) {
-    // the shortest run is a tile (a part each) in four, two in five
+    // Below 48 tiles a CTA (the shortest run then three) what a run costs is
+    // what the balance gains: 8 x 8 caches of 8192 rows, 28 tiles, took 50.1 us
+    // with two runs a stretch and 49.8 with one; 64 ragged ones, 62 tiles, 162.8
+    // us with these three and 173.2 with one.
     const long long per = quot(total, grid);
-    if (claim && per >= 24 && per < (1LL << 24)) {
-      waves = per < 64 ? 4 : 5;
+    if (claim && per >= kClaimTiles && per < (1LL << 24)) {
+      waves = kMaxWaves;
       runs = waves * S;
     }
   }
@@ -300,15 +303,15 @@ struct PagedRuns {
   __device__ __forceinline__ long long begin(int c) const {
     if (waves == 1) return quot(c * total, runs);
     const int g = c / waves, w = c - g * waves;
-    return (g * 256LL + (w ? share(waves, w) : 0)) * total / (256LL * S);
+    return quot((g * 256LL + share(w)) * total, 256LL * S);
   }
   // the run that cost x lies in: the largest c with begin(c) <= x
   __device__ __forceinline__ int of(long long x) const {
     if (waves == 1) return (int)quot((x + 1) * runs - 1, total);
-    const long long n = ((x + 1) * 256 * S - 1) / total;
+    const long long n = quot((x + 1) * 256 * S - 1, total);
     const int g = (int)(n >> 8), in = (int)(n & 255);
     int w = waves - 1;
-    while (w > 0 && share(waves, w) > in) --w;
+    while (w > 0 && share(w) > in) --w;
     return g * waves + w;
   }
 };
@@ -318,18 +321,6 @@ struct PagedRuns {
 // (empty) tile, so that its outputs are written.
 struct PagedWalk {
   int b, kvh, tile, tiles, end;  // end: the sequence's length
-  __device__ __forceinline__ void load(const PagedParams& p, int KT) {
-    end = b < p.B ? min(max(p.seq_lens[b], 0), p.map.max_len) : 0;
-    tiles = max(1, (end - p.start + KT - 1) / KT);
-  }
-  __device__ __forceinline__ void next_unit(const PagedParams& p, int KT) {
-    tile = 0;
-    if (++kvh == p.Hkv) {
-      kvh = 0;
-      ++b;
-      load(p, KT);
-    }
-  }
 };
 
 template <int D, bool BF16, int NB>
@@ -343,7 +334,12 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
   __shared__ __align__(16) PagedSeg segs[C::STAGES];
   constexpr int FIND = 32 * C::WARPS;  // threads that sum the lengths, a chunk of sequences each
   __shared__ int warp_max[C::WARPS];
-  __shared__ long long warp_sum[C::WARPS], sums[FIND];  // cost of the sequences before a chunk
+  __shared__ long long warp_sum[C::WARPS];
+  __shared__ uint32_t sums[FIND];  // cost of the sequences before a chunk
+  __shared__ int ends[FIND];       // with a sequence to a chunk: its length
+  static_assert(sizeof(full) + sizeof(empty) + sizeof(seg_full) + sizeof(segs) + sizeof(warp_max) + sizeof(warp_sum) +
+                        sizeof(sums) + sizeof(ends) <= C::STATIC,
+                "static shared memory");
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* queries = ring + C::STAGES * C::STAGE;
   float* scratch = reinterpret_cast<float*>(queries + C::STAGES * C::QTILE);
@@ -374,48 +370,90 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
   pdl_launch();
 
   // ---- the cost of the call
-  auto cost_of = [&](int b) {
-    const int end = min(max(p.seq_lens[b], 0), p.map.max_len);
-    return max(1, (end - p.start + C::KT - 1) / C::KT) + kUnitCost;
-  };
   const int chunk = (p.B + FIND - 1) / FIND;
+  auto length_of = [&](int b) { return min(max(p.seq_lens[b], 0), p.map.max_len); };
+  auto tiles_of = [&](int end) { return max(1, (end - p.start + C::KT - 1) / C::KT); };
   const int b_lo = (int)min((long long)threadIdx.x * chunk, (long long)p.B);
   const int b_hi = threadIdx.x < FIND ? min(b_lo + chunk, p.B) : b_lo;
-  long long mine = 0;
-  int most = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int n = cost_of(b);
-    mine += n;
-    most = max(most, n);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  long long incl = mine;
+  long long total = 0;
+  int most = 0;  // the largest cost of a sequence
+  if (p.B <= FIND) {
+    // few sequences: the producer alone looks, four to a lane
+    __syncthreads();
+    if (warp == C::WARPS) {
+      constexpr int EACH = FIND / 32;
+      int n[EACH], mine = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (warp < C::WARPS && lane == 31) {
-    warp_sum[warp] = incl;
-    warp_max[warp] = most;
-  }
-  __syncthreads();
-  long long total = 0, before = incl - mine;
+      for (int k = 0; k < EACH; ++k) {
+        const int b = EACH * lane + k, end = b < p.B ? length_of(b) : 0;
+        n[k] = b < p.B ? tiles_of(end) + kUnitCost : 0;
+        ends[b] = end;
+        mine += n[k];  // below 2^30 / 64 each
+        most = max(most, n[k]);
+      }
+      int incl = mine;
 #pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-    most = max(most, warp_max[w]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      most = __reduce_max_sync(0xffffffffu, most);
+      int before = incl - mine;
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        sums[EACH * lane + k] = before;
+        before += n[k];
+      }
+      __syncwarp();
+    }
+  } else {
+    const int b_lo = (int)min((long long)threadIdx.x * chunk, (long long)p.B);
+    const int b_hi = threadIdx.x < FIND ? min(b_lo + chunk, p.B) : b_lo;
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int n = tiles_of(length_of(b)) + kUnitCost;
+      mine += n;
+      most = max(most, n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (warp < C::WARPS && lane == 31) {
+      warp_sum[warp] = incl;
+      warp_max[warp] = most;
+    }
+    __syncthreads();
+    long long before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+      most = max(most, warp_max[w]);
+    }
+    if (threadIdx.x < FIND) sums[threadIdx.x] = (uint32_t)before;
+    __syncthreads();
   }
-  total *= p.Hkv;
-  const long long units = (long long)p.B * p.Hkv;
-  const PagedRuns runs(total, units, p.grid, p.next_run != nullptr);
-  const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA: a unit each
-  if (threadIdx.x < FIND) sums[threadIdx.x] = before;
-  __syncthreads();
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- producer
+    if (total >= 1LL << 31) {  // more rows than a call takes: hours of work, nothing is written
+      if (c == 0 && lane == 0) record_error(DEV_ERR_ARG, PAGED_SITE_ROWS);
+      total = 0;
+    }
+    total *= p.Hkv;
+    const long long units = (long long)p.B * p.Hkv;
+    const PagedRuns runs(total, units, p.grid, p.next_run != nullptr);
+    const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA: a unit each
+    // sequence at.b's length and tiles
+    auto go_to = [&](PagedWalk& at) {
+      at.end = chunk == 1 ? ends[at.b] : length_of(at.b);
+      at.tiles = tiles_of(at.end);
+    };
     // The first tile of run c and the cost of what the run holds from it on.
     // Tile k of a unit sits kUnitCost + k behind the unit's start; there are at
     // most as many runs as there is cost, so no run inside a unit is without a
@@ -427,17 +465,16 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
       // sequence begin at the total)
       int lo = 0;
 #pragma unroll
-      for (int k = 0; k < FIND; k += 32) lo += __popc(__ballot_sync(0xffffffffu, sums[k + lane] * p.Hkv <= t0));
+      for (int k = 0; k < FIND; k += 32) lo += __popc(__ballot_sync(0xffffffffu, (long long)sums[k + lane] * p.Hkv <= t0));
       long long first = sums[lo - 1];
       at.b = min((lo - 1) * chunk, p.B - 1);
-      for (;;) {
-        const int n = cost_of(at.b);
-        if (t0 < (first + n) * p.Hkv || at.b == p.B - 1) break;
-        first += n;
+      go_to(at);
+      while (t0 >= (first + at.tiles + kUnitCost) * p.Hkv && at.b < p.B - 1) {
+        first += at.tiles + kUnitCost;
         ++at.b;
+        go_to(at);
       }
       first *= p.Hkv;
-      at.load(p, C::KT);
       const int cost = at.tiles + kUnitCost;
       at.kvh = (int)quot(t0 - first, cost);
       const int off = (int)(t0 - first - (long long)at.kvh * cost);  // into the unit
@@ -450,7 +487,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     if (whole) {
       if (c < units) {
         at.b = c / p.Hkv;
-        at.load(p, C::KT);
+        go_to(at);
         at.kvh = c % p.Hkv;
         at.tile = 0;
         left = at.tiles;
@@ -527,7 +564,14 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
           else if (lane == 0) p.cuts[(size_t)at.b * p.Hkv + at.kvh] = cut;
         }
         left -= n + kUnitCost;  // the next unit's own cost too
-        if (left > 0) at.next_unit(p, C::KT);
+        if (left > 0) {
+          at.tile = 0;
+          if (++at.kvh == p.Hkv) {
+            at.kvh = 0;
+            ++at.b;
+            go_to(at);
+          }
+        }
       }
       if (lane == 0 && !p.by_unit && !whole && c < runs.runs) p.cuts[run] = run_cut;
       if (!ok || whole || runs.waves == 1) break;
@@ -815,8 +859,8 @@ __device__ __forceinline__ bool cut_ok(const PagedParams& p, const PagedCut& cut
 }
 
 // The units that a boundary between runs cut: a block joins the parts of the
-// query rows of one of p.cuts, if it is a cut: all of them, or (grid.y = G)
-// one, and then all its warps share the row's parts.  Bound: the latency of three dependent reads.
+// query rows of one of p.cuts, if it is a cut, grid.y blocks those of a unit;
+// with few rows to a block several warps share a row's parts.  Bound: the latency of three dependent reads.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   constexpr int VEC = D / 32, WARPS = 8;
@@ -828,8 +872,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   if (!cut_ok(p, cut)) return;
   const int c0 = cut.first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = gridDim.y > 1 ? 1 : p.G, r_lo = blockIdx.y;  // this block's rows
-  const int split = max(1, WARPS / rows);                       // warps of a row
+  const int each = (p.G + gridDim.y - 1) / gridDim.y, r_lo = blockIdx.y * each;
+  const int rows = min(each, p.G - r_lo);  // this block's rows
+  if (rows <= 0) return;
+  const int split = max(1, WARPS / rows);  // warps of a row
   const int sub = warp % split, own = cut.last - c0 + 1, per = (own + split - 1) / split, s0 = min(sub * per, own);
   const size_t row0 = (size_t)cut.b * p.Hq + cut.kvh * p.G;
   for (int r = r_lo + warp / split; r < r_lo + rows; r += WARPS / split) {
