@@ -505,23 +505,31 @@ def _same_device(first, *ts):
     return first.get_device()
 
 
-def _on(device, stream, call):
-    """``call(raw stream)`` with ``device`` current, and on ``stream`` if one
-    is given, so that what is allocated inside belongs to the stream that the
-    kernels run on."""
+def _on(device, stream, call, *args):
+    """``call(raw stream, *args)`` with ``device`` current, and on ``stream``
+    if one is given, so that what is allocated inside belongs to the stream
+    that the kernels run on."""
     import torch
     if stream is None:
         if torch.cuda.current_device() == device:
-            return call(torch.cuda.current_stream(device).cuda_stream)
+            return call(_raw_stream(device), *args)
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream(device).cuda_stream)
+            return call(_raw_stream(device), *args)
     if not hasattr(stream, "cuda_stream"):
         raw = int(stream)
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
     if stream.device.index != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call(stream.cuda_stream, *args)
+
+
+def _raw_stream(device):
+    """The current stream of a device as a number (without the torch object
+    where this torch has the call: 1.2 us a time)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _int32(t, what, shape=None):
@@ -634,35 +642,39 @@ def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, bac
     q_out, k_out = (None, None) if out is None else (out, None) if isinstance(out, torch.Tensor) else out
     if out is not None and (q_out is None or (k is None) != (k_out is None)):
         raise ValueError("out must give a tensor for each input")
-    dev, dt, rot, B, S, D, nseq, pos_stride, rows, empty = _known(
-        ("rope", _sig(q), _sig(k), _sig(freqs), _sig(positions), _sig(cu_seqlens), _sig(q_out), _sig(k_out)),
-        _rope_layout, q, k, freqs, positions, cu_seqlens, (q_out, k_out))
-
-    def call(raw):
-        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        xp, yp = q.data_ptr(), yq.data_ptr()
-        x, y = _ROWS.pack(xp, *rows[0][0]), _ROWS.pack(yp, *rows[0][1])
-        yk = None
-        if q_out is not None:
-            _apart(xp, yp, rows[0])
-        if k is not None:
-            yk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-            kp, ykp = k.data_ptr(), yk.data_ptr()
-            x += _ROWS.pack(kp, *rows[1][0])
-            y += _ROWS.pack(ykp, *rows[1][1])
-            if k_out is not None:
-                _apart(kp, ykp, rows[1])
-                if ykp == yp and ykp:
-                    raise ValueError("the two outputs are the same memory")
-        if not empty:
-            st = _lib.fa_rope(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions),
-                              pos_stride, _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
-            if st != FA_OK:
-                raise FAError(st, "fa_rope")
-        return yq, yk
-
+    known = _known(("rope", _sig(q), _sig(k), _sig(freqs), _sig(positions), _sig(cu_seqlens), _sig(q_out), _sig(k_out)),
+                   _rope_layout, q, k, freqs, positions, cu_seqlens, (q_out, k_out))
     load_library()
-    return _on(dev, stream, call)
+    return _on(known[0], stream, _rope_call, known, q, k, freqs, positions, cu_seqlens, interleaved, amp, q_out, k_out,
+               backward)
+
+
+def _rope_call(raw, known, q, k, freqs, positions, cu_seqlens, interleaved, amp, yq, yk, backward):
+    import torch
+    _, dt, rot, B, S, D, nseq, pos_stride, rows, empty = known
+    given = yq is not None
+    if not given:
+        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None:
+            yk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    xp, yp = q.data_ptr(), yq.data_ptr()
+    x, y = _ROWS.pack(xp, *rows[0][0]), _ROWS.pack(yp, *rows[0][1])
+    if given:
+        _apart(xp, yp, rows[0])
+    if k is not None:
+        kp, ykp = k.data_ptr(), yk.data_ptr()
+        x += _ROWS.pack(kp, *rows[1][0])
+        y += _ROWS.pack(ykp, *rows[1][1])
+        if given:
+            _apart(kp, ykp, rows[1])
+            if ykp == yp and ykp:
+                raise ValueError("the two outputs are the same memory")
+    if not empty:
+        st = _lib.fa_rope(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions),
+                          pos_stride, _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
+        if st != FA_OK:
+            raise FAError(st, "fa_rope")
+    return yq, yk
 
 
 def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved: bool = False, amp: float = 1.0, out=None,
@@ -755,32 +767,35 @@ def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
     length 0 and tokens behind the last sequence write nothing; a row past
     the table or a page outside the pool is reported by
     ``check_device_error``."""
-    import torch
-    dev, dt, B, T, D, pages, k_rows, v_rows, q_rows, rot = _known(
+    known = _known(
         ("append", _sig(k), _sig(v), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), _sig(cu_seqlens),
          _sig(q), _sig(freqs), _sig(positions), _sig(q_out)),
         _append_layout, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
-
-    def call(raw):
-        to, qx, qy = q_out, None, None
-        if q is not None:
-            if q_out is None:
-                to = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            xp, yp = q.data_ptr(), to.data_ptr()
-            if q_out is not None:
-                _apart(xp, yp, q_rows)
-            qx, qy = _ROWS.pack(xp, *q_rows[0]), _ROWS.pack(yp, *q_rows[1])
-        if T and B:
-            st = _lib.fa_append_paged(_ROWS.pack(k.data_ptr(), *k_rows), _ROWS.pack(v.data_ptr(), *v_rows), qx, qy,
-                                      _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(),
-                                      _ptr(cu_seqlens), B, T, _ptr(freqs), rot, interleaved, amp, _ptr(positions), D,
-                                      dt, raw)
-            if st != FA_OK:
-                raise FAError(st, "fa_append_paged")
-        return to
-
     load_library()
-    return _on(dev, stream, call)
+    return _on(known[0], stream, _append_call, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q,
+               freqs, positions, interleaved, amp, q_out)
+
+
+def _append_call(raw, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions,
+                 interleaved, amp, q_out):
+    import torch
+    _, dt, B, T, D, pages, k_rows, v_rows, q_rows, rot = known
+    to, qx, qy = q_out, None, None
+    if q is not None:
+        if q_out is None:
+            to = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        xp, yp = q.data_ptr(), to.data_ptr()
+        if q_out is not None:
+            _apart(xp, yp, q_rows)
+        qx, qy = _ROWS.pack(xp, *q_rows[0]), _ROWS.pack(yp, *q_rows[1])
+    if T and B:
+        st = _lib.fa_append_paged(_ROWS.pack(k.data_ptr(), *k_rows), _ROWS.pack(v.data_ptr(), *v_rows), qx, qy,
+                                  _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(),
+                                  _ptr(cu_seqlens), B, T, _ptr(freqs), rot, interleaved, amp, _ptr(positions), D, dt,
+                                  raw)
+        if st != FA_OK:
+            raise FAError(st, "fa_append_paged")
+    return to
 
 
 def _decode_layout(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, out, lse, workspace):
@@ -812,31 +827,36 @@ def _decode_layout(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefi
 
 def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, out, lse, workspace,
                   stream):
-    import torch
-    dev, dt, B, Hq, D, pages, need, size = _known(
+    known = _known(
         ("decode", _sig(q), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), prefix_len,
          _sig(prefix_table), _sig(out), _sig(lse), _sig(workspace)),
         _decode_layout, q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, out, lse, workspace)
+    load_library()
+    return _on(known[0], stream, _decode_call, known, q, k_pages, v_pages, block_table, seq_lens, prefix_len,
+               prefix_table, scale, out, lse, workspace)
+
+
+def _decode_call(raw, known, q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, o, lse, ws):
+    import torch
+    _, dt, B, Hq, D, pages, need, size = known
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-
-    def call(raw):
-        o = torch.empty_like(q) if out is None else out
-        ll = torch.empty((B, Hq), device=q.device, dtype=torch.float32) if lse is None else lse
-        ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8) if workspace is None else workspace
-        at = _pack_pages(k_pages, v_pages, block_table, pages)
-        if prefix_len:
-            st = _lib.fa_decode_prefix(q.data_ptr(), at, seq_lens.data_ptr(), prefix_len, _ptr(prefix_table),
-                                       o.data_ptr(), ll.data_ptr(), B, Hq, D, scale, dt, ws.data_ptr(), size, raw)
-        else:
-            st = _lib.fa_decode_paged(q.data_ptr(), at, seq_lens.data_ptr(), o.data_ptr(), ll.data_ptr(), B, Hq, D,
-                                      scale, dt, ws.data_ptr(), size, raw)
-        if st != FA_OK:
-            raise FAError(st, "fa_decode_prefix" if prefix_len else "fa_decode_paged")
-        return o, ll
-
-    load_library()
-    return _on(dev, stream, call)
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+    if ws is None:
+        ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    at = _pack_pages(k_pages, v_pages, block_table, pages)
+    if prefix_len:
+        st = _lib.fa_decode_prefix(q.data_ptr(), at, seq_lens.data_ptr(), prefix_len, _ptr(prefix_table), o.data_ptr(),
+                                   lse.data_ptr(), B, Hq, D, scale, dt, ws.data_ptr(), size, raw)
+    else:
+        st = _lib.fa_decode_paged(q.data_ptr(), at, seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, D, scale,
+                                  dt, ws.data_ptr(), size, raw)
+    if st != FA_OK:
+        raise FAError(st, "fa_decode_prefix" if prefix_len else "fa_decode_paged")
+    return o, lse
 
 
 def decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float | None = None, out=None, lse=None,
