@@ -205,8 +205,13 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
   }
   const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
   if (s != FA_OK) return s;
-  if (p.n_pre)
-    return launch_after(fa::paged_join_kernel<D, BF16>, dim3((unsigned)(((long long)p.B * p.Hq + 7) / 8)), 256, 0, st, a);
+  if (p.n_pre) {
+    // four warps a row while all of them run at once (eight blocks to an SM)
+    const long long rows = (long long)p.B * p.Hq;
+    if (rows <= 16LL * sm_count() && p.n_pre >= 4)
+      return launch_after(fa::paged_join_kernel<D, BF16, 4>, dim3((unsigned)((rows + 1) / 2)), 256, 0, st, a);
+    return launch_after(fa::paged_join_kernel<D, BF16, 1>, dim3((unsigned)((rows + 7) / 8)), 256, 0, st, a);
+  }
   // units that are never cut: of one tile, or all of them short and on an SM of their own
   if (tiles == 1 || (tiles <= fa::kWholeTiles && units <= a.grid)) return FA_OK;
   // few rows to a block (and so many warps to a row) as long as the blocks, three

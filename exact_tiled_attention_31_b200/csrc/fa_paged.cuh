@@ -902,35 +902,59 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
   store_row<VEC, BF16>(p, row0 + r_lo + warp / split, D, lane, all);
 }
 
-// Every row's shared rows' parts and its own, whole or cut: a warp per row.
-// Bound: the n_pre + 1 fp32 parts of every row read once, from L2 mostly.
-// (Joining inside paged_kernel put these loads' latency into every unit's
-// chain: 5 us a unit with 9 parts.)
-template <int D, bool BF16>
+// Every row's shared rows' parts and its own, whole or cut: SPLIT warps per row,
+// each a share of the parts.  Bound: the n_pre + 1 fp32 parts of every row read
+// once, from L2 mostly; with few rows their latency, hence the split (2048 rows
+// of 17 parts took 8 us with a warp each, 14 warps to an SM).  (Joining inside
+// paged_kernel put this latency into every unit's chain: 5 us a unit with 9
+// parts.)
+template <int D, bool BF16, int SPLIT>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
-  constexpr int VEC = D / 32;
+  constexpr int VEC = D / 32, ROWS = 8 / SPLIT;
+  __shared__ __align__(16) float s_o[8][D];
+  __shared__ float s_l[8];
   pdl_wait();
   pdl_launch();
-  const int lane = threadIdx.x & 31;
-  const size_t rows = (size_t)p.B * p.Hq, row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int b = (int)(row / p.Hq), h = (int)(row % p.Hq), kvh = h / p.G, r = h - kvh * p.G;
-  const PagedCut cut = p.cuts[(size_t)b * p.Hkv + kvh];
-  const bool is_cut = cut_ok(p, cut);
-  const int c0 = cut.first, own = is_cut ? cut.last - c0 + 1 : 1;
-  auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % SPLIT;
+  const size_t rows = (size_t)p.B * p.Hq, row = (size_t)blockIdx.x * ROWS + warp / SPLIT;
+  const bool in = row < rows;
   RowSum<VEC> sum;
-  add_parts<VEC>(
-      sum, p.n_pre + own, lane,
-      [&](int s) {
-        return s < p.n_pre ? p.pre_lse[s * rows + row] : is_cut ? p.lse_part[slot(s - p.n_pre)] : p.own_lse[row];
-      },
-      [&](int s) {
-        return s < p.n_pre ? p.pre_o + (s * rows + row) * D
-               : is_cut    ? p.o_part + slot(s - p.n_pre) * D
-                           : p.own_o + row * D;
-      });
-  store_row<VEC, BF16>(p, row, D, lane, sum);
+  if (in) {
+    const int b = (int)(row / p.Hq), h = (int)(row % p.Hq), kvh = h / p.G, r = h - kvh * p.G;
+    const PagedCut cut = p.cuts[(size_t)b * p.Hkv + kvh];
+    const bool is_cut = cut_ok(p, cut);
+    const int c0 = cut.first, n = p.n_pre + (is_cut ? cut.last - c0 + 1 : 1);
+    const int per = (n + SPLIT - 1) / SPLIT, s0 = min(sub * per, n);
+    auto slot = [&](int s) { return (size_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * p.G + r; };
+    add_parts<VEC>(
+        sum, min(per, n - s0), lane,
+        [&](int i) {
+          const int s = s0 + i;
+          return s < p.n_pre ? p.pre_lse[s * rows + row] : is_cut ? p.lse_part[slot(s - p.n_pre)] : p.own_lse[row];
+        },
+        [&](int i) {
+          const int s = s0 + i;
+          return s < p.n_pre ? p.pre_o + (s * rows + row) * D
+                 : is_cut    ? p.o_part + slot(s - p.n_pre) * D
+                             : p.own_o + row * D;
+        });
+    if constexpr (SPLIT == 1) {
+      store_row<VEC, BF16>(p, row, D, lane, sum);
+    } else {
+      const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sum.o[i] *= inv;
+      store_vec<VEC>(&s_o[warp][VEC * lane], sum.o);
+      if (lane == 0) s_l[warp] = sum.w == 0.f ? -INFINITY : sum.m + __log2f(sum.w);
+    }
+  }
+  if constexpr (SPLIT > 1) {
+    __syncthreads();
+    if (sub || !in) return;
+    RowSum<VEC> all;
+    add_parts<VEC>(all, SPLIT, lane, [&](int s) { return s_l[warp + s]; }, [&](int s) { return s_o[warp + s]; });
+    store_row<VEC, BF16>(p, row, D, lane, all);
+  }
 }
 
 }  // namespace fa

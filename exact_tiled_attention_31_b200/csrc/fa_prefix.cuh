@@ -38,6 +38,17 @@ struct PrefixParams {
   float scale_log2;
 };
 
+// `bytes` (a multiple of 16) of shared memory that this thread wrote (and
+// fenced) to global memory, and the wait for all of this thread's copies.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(768, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -336,14 +347,49 @@ __global__ void __launch_bounds__(768, 1)
       lr = lr * alpha + ((r0 + r1) + (r2 + r3));
       m = m_new;
     }
+    // ---- normalised fp32 parts and the log2 of the fp32 sums: each warp its 32
+    // rows and half of the columns, through the tile buffers (free once every
+    // product of both tiles is done) in rows 16 bytes apart from a bank
+    // conflict, and out as one bulk copy per row half.  (Four warps storing
+    // from registers, a row a lane, took 6.5 us.)
     if (ok && n_t > 0) {
       sum_buf[((2 * t + h) * 2 + 0) * 128 + r] = l;
       sum_buf[((2 * t + h) * 2 + 1) * 128 + r] = lr;
       mbar_arrive(&stats_ready[t]);
+      ok = __all_sync(0xffffffffu, mbar_wait(&stats_ready[t], 0, FWD_SITE_ST) && mbar_wait(&o_full[0], 0, FWD_SITE_O) &&
+                                       (!has_t1 || mbar_wait(&o_full[1], 0, FWD_SITE_O)));
+      if (ok) {
+        tc_fence_after();
+        const float lt = l + sum_buf[((2 * t + (h ^ 1)) * 2 + 0) * 128 + r];
+        const float lrt = lr + sum_buf[((2 * t + (h ^ 1)) * 2 + 1) * 128 + r];
+        const float inv = lrt == 0.f ? 0.f : 1.f / lrt;
+        constexpr int HALF = D / 2, STRIDE = D * 4 + 16;
+        static_assert(256 * STRIDE <= C::BAR_OFF, "parts fit the tile buffers");
+        uint8_t* out = smem + (128 * t + r) * STRIDE + h * HALF * 4;
+        const uint32_t tO = tmem + lane_off + C::TM_O + D * t + HALF * h;
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + 32 * c, ov);
+          tmem_ld_wait(ov);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(out)[8 * c + i] =
+                make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+        }
+        fence_proxy_async_smem();
+        if (b >= 0) {
+          const size_t row = (size_t)split * p.B * p.Hq + (size_t)b * p.Hq + kvh * p.G + r % p.G;
+          bulk_store(p.pre_o + row * D + h * HALF, out, HALF * 4);
+          if (h == 0) p.pre_lse[row] = lt == 0.f ? -INFINITY : m + __log2f(lt);
+        }
+        bulk_store_wait();
+      }
     }
   } else {
     regs_dec<48>();
-    // ------------------------------------------------------------ correction + parts
+    // ------------------------------------------------------------ correction
     const int r = 32 * (warp & 3) + (int)lane;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = p.scale_log2;
@@ -384,35 +430,6 @@ __global__ void __launch_bounds__(768, 1)
         tc_fence_before();
         mbar_arrive(&o_ready[t]);
       }
-    }
-    // ---- normalised fp32 parts and the log2 of the fp32 sums
-    for (int t = 0; t < 2 && ok; ++t) {
-      if ((t ? n1 : n0) == 0) continue;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(&stats_ready[t], 0, FWD_SITE_ST) && mbar_wait(&o_full[t], 0, FWD_SITE_O));
-      if (!ok) break;
-      tc_fence_after();
-      const float m = t ? m_row1 : m_row0;
-      const float l = sum_buf[((2 * t + 0) * 2 + 0) * 128 + r] + sum_buf[((2 * t + 1) * 2 + 0) * 128 + r];
-      const float lr = sum_buf[((2 * t + 0) * 2 + 1) * 128 + r] + sum_buf[((2 * t + 1) * 2 + 1) * 128 + r];
-      const float inv = lr == 0.f ? 0.f : 1.f / lr;
-      const int b = seq_of_row(t, r);
-      const size_t row = (size_t)split * p.B * p.Hq + (size_t)max(b, 0) * p.Hq + kvh * p.G + r % p.G;
-      float4* dst = reinterpret_cast<float4*>(p.pre_o + row * D);
-      const uint32_t tO = tmem + lane_off + C::TM_O + D * t;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t ov[16];
-        tmem_ld16(tO + 16 * c, ov);
-        tmem_ld_wait(ov);
-        if (b >= 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[4 * c + i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                                         __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
-        }
-      }
-      if (b >= 0) p.pre_lse[row] = l == 0.f ? -INFINITY : m + __log2f(l);
     }
   }
 
