@@ -64,38 +64,23 @@ fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, 
 }
 
 // ---------------------------------------------------------------- rotary positions
-// Heads a block walks over: all of them share a token's sines and cosines, but
-// below about eight blocks per SM a block takes fewer, down to one batch of
-// loads, so that few tokens still spread over the SMs.
-int heads_per_block(long long token_blocks, int heads) {
-  const long long want = 8LL * sm_count();
-  const long long groups = std::max(1LL, std::min<long long>((want + token_blocks - 1) / token_blocks,
-                                                             (heads + fa::kRopeBatch - 1) / fa::kRopeBatch));
-  const int per = (int)((heads + groups - 1) / groups);
-  return (per + fa::kRopeBatch - 1) / fa::kRopeBatch * fa::kRopeBatch;
-}
-
 template <int D, bool BF16>
-fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
+fa_status launch_rope(const fa::RopeParams& p, bool inter, cudaStream_t st) {
   constexpr int TOKENS = fa::kRopeThreads / (D / 16);
   const long long blocks = ((long long)p.B * p.S + TOKENS - 1) / TOKENS;
   const int heads = p.heads[0] + p.heads[1];
-  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  p.per = heads_per_block(blocks, heads);
-  const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
-  if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)p.B * p.S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (heads + fa::kRopeHeads - 1) / fa::kRopeHeads);
   return launch_after(inter ? fa::rope_kernel<D, BF16, true> : fa::rope_kernel<D, BF16, false>, grid, fa::kRopeThreads,
                       0, st, p);
 }
 
 template <int D, bool BF16>
-fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
+fa_status launch_append(const fa::AppendParams& p, bool inter, cudaStream_t st) {
   constexpr int TOKENS = fa::kRopeThreads / (D / 16);
   const long long blocks = ((long long)p.T + TOKENS - 1) / TOKENS;
   const int heads = p.Hq + 2 * p.Hkv;
-  p.per = heads_per_block(blocks, heads);
-  const dim3 grid((unsigned)blocks, (heads + p.per - 1) / p.per);
-  if (grid.y > 65535) return FA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (heads + fa::kRopeHeads - 1) / fa::kRopeHeads);
   return launch_after(inter ? fa::append_kernel<D, BF16, true> : fa::append_kernel<D, BF16, false>, grid,
                       fa::kRopeThreads, 0, st, p);
 }

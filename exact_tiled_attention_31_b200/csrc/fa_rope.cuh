@@ -10,13 +10,19 @@
 // Angles.  pos * f_i reaches 10^6 radians and more, where fp32 has lost the
 // phase.  The turns pos * f_i / 2 pi are formed in fp64 and reduced to
 // [-1/2, 1/2] there (error below 2^-34 turns up to position 2^20, 2^-23 at
-// 2^31); only the reduced turns go to fp32, for sincospif.
+// 2^31).  The reduced angle goes to fp32 and to the special-function unit's
+// sine and cosine, whose error on [-pi, pi] is below 2^-21 (with the angle's
+// own rounding the pair is off by at most 2^-20 of its length, 2^-9 of the
+// half step of fp16; sincospif, 40 instructions instead of 3, was no closer
+// after the rounding to 16 bits).
 //
 // Bound: HBM.  Every row is read once and written once, 2 x 2 D bytes, with
 // three multiply-adds a pair.  A thread owns two 8-column chunks of one
 // token that hold whole pairs (columns c and c + R/2 of the rotated part;
-// likewise of the copied part), forms their eight sines and cosines once and
-// then walks over the token's heads, four heads' loads at a time in flight.
+// likewise of the copied part) for four heads, all of whose loads are in
+// flight before it forms the eight sines and cosines.  Four heads to a block,
+// not more: the angles are cheap, and many short blocks leave a short tail
+// (eight heads a block in 2.3 waves: 24.0 us for q and k of 32 heads x 4096).
 #pragma once
 
 #include "sm100.cuh"
@@ -24,7 +30,7 @@
 namespace fa {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;  // heads whose loads a thread keeps in flight
+constexpr int kRopeHeads = 4;  // heads of a block, all in flight
 
 // A strided stack of rows of D contiguous 16-bit values (strides in elements).
 struct RowsIn {
@@ -51,10 +57,9 @@ __device__ __forceinline__ int seq_of(const int* cu, int nseq, int t) {
 __device__ __forceinline__ void rope_angle(double freq, int pos, float amp, float& c, float& s) {
   double turns = (double)pos * (freq * 0.15915494309189533577);
   turns -= rint(turns);
-  float sn, cs;
-  sincospif(2.f * (float)turns, &sn, &cs);
-  c = cs * amp;
-  s = sn * amp;
+  const float x = (float)turns * 6.2831853071795865f;
+  c = __cosf(x) * amp;
+  s = __sinf(x) * amp;
 }
 
 // The two 8-column chunks of item `it` (of D / 16 items), whether they are
@@ -102,7 +107,7 @@ struct RopeParams {
   const int* positions;    // [B, S] by pos_batch, or null: the index in the sequence
   long long pos_batch;
   const int* cu;           // packed batch (B = 1, S rows): [nseq + 1] offsets, or null
-  int nseq, B, S, R, per;  // per: heads a block walks over
+  int nseq, B, S, R;
   float amp;
   float sign;              // -1 turns back
 };
@@ -114,9 +119,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
-  const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;
-  if (n >= (long long)p.B * p.S) return;
-  const int b = (int)(n / p.S), t = (int)(n - (long long)b * p.S);
+  const uint32_t n = blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  if (n >= (uint32_t)p.B * (uint32_t)p.S) return;
+  const int b = n / (uint32_t)p.S, t = n - b * (uint32_t)p.S;
   int pos = t;
   if (p.cu) {
     const int s = seq_of(p.cu, p.nseq, t);
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   }
   if (p.positions) pos = p.positions[b * p.pos_batch + t];
   const RopeItem<D, INTER> item(it, p.R);
-  const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads[0] + p.heads[1]);
+  const int h0 = blockIdx.y * kRopeHeads, h1 = min(h0 + kRopeHeads, p.heads[0] + p.heads[1]);
   // head h of both tensors' heads in one row: h < heads[0] is the first's
   auto in = [&](int h) {
     const int w = h >= p.heads[0];
@@ -135,32 +140,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     const int w = h >= p.heads[0];
     return p.y[w].p + b * p.y[w].batch + (long long)(h - (w ? p.heads[0] : 0)) * p.y[w].head + t * p.y[w].row;
   };
-  uint4 lo[kRopeBatch], hi[kRopeBatch];
-  float c[8], s[8];
-  for (int h = h0; h < h1; h += kRopeBatch) {
+  uint4 lo[kRopeHeads], hi[kRopeHeads];
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k)
-      if (h + k < h1) {
-        const uint16_t* x = in(h + k);
-        lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
-        hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
-      }
-    if (h == h0 && item.turn) {  // while the first loads are on their way
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
-        s[j] *= p.sign;
-      }
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (h0 + k < h1) {
+      const uint16_t* x = in(h0 + k);
+      lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
+      hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
     }
+  float c[8], s[8];
+  if (item.turn) {
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k)
-      if (h + k < h1) {
-        if (item.turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
-        uint16_t* y = out(h + k);
-        *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
-        *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
-      }
+    for (int j = 0; j < 8; ++j) {
+      rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
+      s[j] *= p.sign;
+    }
   }
+#pragma unroll
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (h0 + k < h1) {
+      if (item.turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+      uint16_t* y = out(h0 + k);
+      *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
+      *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -190,7 +193,7 @@ struct AppendParams {
   const double* freqs;     // null (R = 0): no rotation
   const int* positions;    // [T], or null
   int n_pages, page_shift, max_pages;
-  int nseq, T, Hq, Hkv, R, per;
+  int nseq, T, Hq, Hkv, R;
   float amp;
 };
 
@@ -200,9 +203,9 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
-  const long long n = (long long)blockIdx.x * TOKENS + threadIdx.x / ITEMS;
-  if (n >= p.T) return;
-  const int t = (int)n;
+  const uint32_t n = blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  if (n >= (uint32_t)p.T) return;
+  const int t = n;
   int b = t, i;
   if (p.cu) {
     b = seq_of(p.cu, p.nseq, t);
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   const RopeItem<D, INTER> item(it, p.R);
   // heads in one row: q's Hq, k's Hkv, v's Hkv
   const int hk = p.Hq, hv = p.Hq + p.Hkv;
-  const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, hv + p.Hkv);
+  const int h0 = blockIdx.y * kRopeHeads, h1 = min(h0 + kRopeHeads, hv + p.Hkv);
   auto in = [&](int h) {
     return h < hk   ? p.q.p + h * p.q.head + t * p.q.row
            : h < hv ? p.k.p + (h - hk) * p.k.head + t * p.k.row
@@ -233,32 +236,30 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
     const long long off = at + ((long long)(h < hv ? h - hk : h - hv) << p.page_shift) * D;
     return (h < hv ? p.k_pages : p.v_pages) + off;
   };
-  uint4 lo[kRopeBatch], hi[kRopeBatch];
-  float c[8], s[8];
-  for (int h = h0; h < h1; h += kRopeBatch) {
+  uint4 lo[kRopeHeads], hi[kRopeHeads];
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k)
-      if (h + k < h1) {
-        const uint16_t* x = in(h + k);
-        lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
-        hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
-      }
-    if (h == h0 && item.turn && h < hv) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (h0 + k < h1) {
+      const uint16_t* x = in(h0 + k);
+      lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
+      hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
     }
+  float c[8], s[8];
+  if (item.turn && h0 < hv) {
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k)
-      if (h + k < h1) {
-        if (item.turn && h + k < hv) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
-        uint16_t* y = out(h + k);
-        if (y) {
-          *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
-          *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
-        }
-      }
+    for (int j = 0; j < 8; ++j)
+      rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
   }
+#pragma unroll
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (h0 + k < h1) {
+      if (item.turn && h0 + k < hv) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+      uint16_t* y = out(h0 + k);
+      if (y) {
+        *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
+        *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
+      }
+    }
 }
 
 }  // namespace fa
