@@ -64,23 +64,28 @@ fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, 
 }
 
 // ---------------------------------------------------------------- rotary positions
-template <int D, bool BF16>
-fa_status launch_rope(const fa::RopeParams& p, bool inter, cudaStream_t st) {
+// Blocks of `rows` tokens of `heads` heads, the heads' index first where the
+// heads of a token are nearer than its neighbours (and the tokens' fits second).
+template <int D>
+dim3 rope_grid(long long rows, int heads, long long head_stride, long long row_stride, bool& heads_near) {
   constexpr int TOKENS = fa::kRopeThreads / (D / 16);
-  const long long blocks = ((long long)p.B * p.S + TOKENS - 1) / TOKENS;
-  const int heads = p.heads[0] + p.heads[1];
+  const unsigned tiles = (unsigned)((rows + TOKENS - 1) / TOKENS);
+  const unsigned groups = (heads + fa::kRopeHeads - 1) / fa::kRopeHeads;
+  heads_near = head_stride < row_stride && tiles <= 65535;
+  return heads_near ? dim3(groups, tiles) : dim3(tiles, groups);
+}
+
+template <int D, bool BF16>
+fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
   if ((long long)p.B * p.S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks, (heads + fa::kRopeHeads - 1) / fa::kRopeHeads);
+  const dim3 grid = rope_grid<D>((long long)p.B * p.S, p.heads[0] + p.heads[1], p.x[0].head, p.x[0].row, p.heads_near);
   return launch_after(inter ? fa::rope_kernel<D, BF16, true> : fa::rope_kernel<D, BF16, false>, grid, fa::kRopeThreads,
                       0, st, p);
 }
 
 template <int D, bool BF16>
-fa_status launch_append(const fa::AppendParams& p, bool inter, cudaStream_t st) {
-  constexpr int TOKENS = fa::kRopeThreads / (D / 16);
-  const long long blocks = ((long long)p.T + TOKENS - 1) / TOKENS;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const dim3 grid((unsigned)blocks, (heads + fa::kRopeHeads - 1) / fa::kRopeHeads);
+fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
+  const dim3 grid = rope_grid<D>(p.T, p.Hq + 2 * p.Hkv, p.k.head, p.k.row, p.heads_near);
   return launch_after(inter ? fa::append_kernel<D, BF16, true> : fa::append_kernel<D, BF16, false>, grid,
                       fa::kRopeThreads, 0, st, p);
 }

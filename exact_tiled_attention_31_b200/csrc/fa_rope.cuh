@@ -21,15 +21,19 @@
 // token that hold whole pairs (columns c and c + R/2 of the rotated part;
 // likewise of the copied part) for four heads, all of whose loads are in
 // flight before it forms the eight sines and cosines.  Four heads to a block,
-// not more: the angles are cheap, and many short blocks leave a short tail
-// (eight heads a block in 2.3 waves: 24.0 us for q and k of 32 heads x 4096).
+// and 128 threads, not more: the angles are cheap, and many short blocks leave
+// a short tail (q and k of 32 heads x 4096 rows: 24.0 us with 256 threads and
+// eight heads, 23.7 with four, 22.8 with 128 threads).  Where the heads of a
+// token lie next to each other, neighbouring blocks take the heads of the same
+// tokens instead of the next tokens (22.4 us; with rows of a head next to each
+// other that costs 1 %: 81.0 against 80.2 us for 64 heads x 8192 twice).
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeHeads = 4;  // heads of a block, all in flight
 
 // A strided stack of rows of D contiguous 16-bit values (strides in elements).
@@ -108,18 +112,20 @@ struct RopeParams {
   long long pos_batch;
   const int* cu;           // packed batch (B = 1, S rows): [nseq + 1] offsets, or null
   int nseq, B, S, R;
+  bool heads_near;         // grid: (head groups, token tiles) instead of (token tiles, head groups)
   float amp;
   float sign;              // -1 turns back
 };
 
-// grid: (token tiles, head groups); block: tokens x D / 16 items
+// block: tokens x D / 16 items
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   pdl_wait();
   pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
-  const uint32_t n = blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  const uint32_t tile = p.heads_near ? blockIdx.y : blockIdx.x, group = p.heads_near ? blockIdx.x : blockIdx.y;
+  const uint32_t n = tile * TOKENS + threadIdx.x / ITEMS;
   if (n >= (uint32_t)p.B * (uint32_t)p.S) return;
   const int b = n / (uint32_t)p.S, t = n - b * (uint32_t)p.S;
   int pos = t;
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   }
   if (p.positions) pos = p.positions[b * p.pos_batch + t];
   const RopeItem<D, INTER> item(it, p.R);
-  const int h0 = blockIdx.y * kRopeHeads, h1 = min(h0 + kRopeHeads, p.heads[0] + p.heads[1]);
+  const int h0 = group * kRopeHeads, h1 = min(h0 + kRopeHeads, p.heads[0] + p.heads[1]);
   // head h of both tensors' heads in one row: h < heads[0] is the first's
   auto in = [&](int h) {
     const int w = h >= p.heads[0];
@@ -194,6 +200,7 @@ struct AppendParams {
   const int* positions;    // [T], or null
   int n_pages, page_shift, max_pages;
   int nseq, T, Hq, Hkv, R;
+  bool heads_near;         // as in RopeParams
   float amp;
 };
 
@@ -203,7 +210,8 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   pdl_launch();
   constexpr int ITEMS = D / 16, TOKENS = kRopeThreads / ITEMS;
   const int it = threadIdx.x % ITEMS;
-  const uint32_t n = blockIdx.x * TOKENS + threadIdx.x / ITEMS;
+  const uint32_t tile = p.heads_near ? blockIdx.y : blockIdx.x, group = p.heads_near ? blockIdx.x : blockIdx.y;
+  const uint32_t n = tile * TOKENS + threadIdx.x / ITEMS;
   if (n >= (uint32_t)p.T) return;
   const int t = n;
   int b = t, i;
@@ -219,12 +227,12 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   const int slot = i >> p.page_shift, row = i & ((1 << p.page_shift) - 1);
   const int page = slot < p.max_pages ? p.table[b * p.table_stride + slot] : -1;
   const bool placed = page >= 0 && page < p.n_pages;
-  if (!placed && it == 0 && blockIdx.y == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
+  if (!placed && it == 0 && group == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
   const long long at = placed ? page * p.page_stride + (long long)row * D : 0;
   const RopeItem<D, INTER> item(it, p.R);
   // heads in one row: q's Hq, k's Hkv, v's Hkv
   const int hk = p.Hq, hv = p.Hq + p.Hkv;
-  const int h0 = blockIdx.y * kRopeHeads, h1 = min(h0 + kRopeHeads, hv + p.Hkv);
+  const int h0 = group * kRopeHeads, h1 = min(h0 + kRopeHeads, hv + p.Hkv);
   auto in = [&](int h) {
     return h < hk   ? p.q.p + h * p.q.head + t * p.q.row
            : h < hv ? p.k.p + (h - hk) * p.k.head + t * p.k.row
