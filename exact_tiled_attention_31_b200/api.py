@@ -542,7 +542,7 @@ def _contiguous(shape):
     st, n = [], 1
     for s in reversed(shape):
         st.append(n)
-        n *= s
+        n *= max(s, 1)
     return tuple(reversed(st))
 
 
