@@ -263,11 +263,6 @@ constexpr int kMinRun = 4;
 // From this many tiles a CTA on runs are handed out.
 constexpr long long kClaimTiles = 48;
 
-// floor(a / b), b > 0, a >= 0: by 32-bit division where both fit
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
 // The cost Hkv * sum_b (tiles(b) + kUnitCost) of a call, cut into runs.  CTAs do
 // not stream equally fast: on B200 whole groups of SMs get up to 8 % less than
 // the mean, others 8 % more (32 x 8 caches of 8192 rows in equal runs: the
@@ -280,38 +275,45 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 // end of the list its last units came in up to a hundred parts, and joining
 // them cost more than the balance gained.)
 struct PagedRuns {
-  long long total;
-  int S, runs, waves;  // CTAs; runs in all; runs of a stretch (1: `runs` equal ones)
+  int total;               // below 2^31: what begin() forms in 32 bits
+  int S, runs, waves;      // CTAs; runs in all; runs of a stretch (1: `runs` equal ones)
+  uint32_t quot, rest;     // one run a stretch: total = quot * runs + rest
+  uint64_t step;           // several: cost of a 256th of a stretch, in 65536ths
   static constexpr int kMaxWaves = 3;
   // where in a stretch its runs begin, in 256ths: they are 208, 32 and 16 long
   static __device__ __forceinline__ int share(int w) { return w == 0 ? 0 : w == 1 ? 208 : 240; }
-  __device__ __forceinline__ PagedRuns(long long total, long long units, int grid, bool claim)
-      : total(total), S(grid), runs((int)min((long long)grid, max(units, total / kMinRun))), waves(1) {
+  __device__ __forceinline__ PagedRuns(int total, long long units, int grid, bool claim)
+      : total(total), S(grid), runs((int)min((long long)grid, max(units, (long long)(total / kMinRun)))), waves(1),
+        step(0) {
     // Below 48 tiles a CTA (the shortest run then three) what a run costs is
     // what the balance gains: 8 x 8 caches of 8192 rows, 28 tiles, took 50.1 us
     // with two runs a stretch and 49.8 with one; 64 ragged ones, 62 tiles, 162.8
     // us with these three and 173.2 with one.
-    const long long per = quot(total, grid);
-    if (claim && per >= kClaimTiles && per < (1LL << 24)) {
+    const uint32_t per = (uint32_t)total / (uint32_t)S;
+    if (claim && per >= kClaimTiles) {
       waves = kMaxWaves;
       runs = waves * S;
+      step = (uint64_t)per * 256 + ((uint32_t)total - per * S) * 256u / (uint32_t)S;
     }
+    quot = (uint32_t)total / (uint32_t)runs;
+    rest = (uint32_t)total - quot * runs;
   }
   // place in the list of the i-th run to be taken
   __device__ __forceinline__ int place(int i) const { return waves == 1 ? i : (i % S) * waves + i / S; }
   // cost in front of run c (by place)
-  __device__ __forceinline__ long long begin(int c) const {
-    if (waves == 1) return quot(c * total, runs);
-    const int g = c / waves, w = c - g * waves;
-    return quot((g * 256LL + share(w)) * total, 256LL * S);
+  __device__ __forceinline__ int begin(int c) const {
+    if (waves == 1) return c * quot + c * rest / (uint32_t)runs;
+    const int g = c / kMaxWaves, w = c - g * kMaxWaves;
+    return c >= runs ? total : (int)(((uint32_t)(g * 256 + share(w)) * step) >> 16);
   }
   // the run that cost x lies in: the largest c with begin(c) <= x
-  __device__ __forceinline__ int of(long long x) const {
-    if (waves == 1) return (int)quot((x + 1) * runs - 1, total);
-    const long long n = quot((x + 1) * 256 * S - 1, total);
-    const int g = (int)(n >> 8), in = (int)(n & 255);
+  __device__ __forceinline__ int of(int x) const {
+    const int n = waves == 1 ? runs : S;
+    int g = min(n - 1, (int)((float)x * ((float)n / (float)total)));  // near
+    while (g > 0 && begin(g * waves) > x) --g;
+    while (g + 1 < n && begin((g + 1) * waves) <= x) ++g;
     int w = waves - 1;
-    while (w > 0 && share(w) > in) --w;
+    while (w > 0 && begin(g * waves + w) > x) --w;
     return g * waves + w;
   }
 };
@@ -441,13 +443,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- producer
+    total *= p.Hkv;
     if (total >= 1LL << 31) {  // more rows than a call takes: hours of work, nothing is written
       if (c == 0 && lane == 0) record_error(DEV_ERR_ARG, PAGED_SITE_ROWS);
       total = 0;
     }
-    total *= p.Hkv;
     const long long units = (long long)p.B * p.Hkv;
-    const PagedRuns runs(total, units, p.grid, p.next_run != nullptr);
+    const PagedRuns runs((int)total, units, p.grid, p.next_run != nullptr);
     const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA: a unit each
     // sequence at.b's length and tiles
     auto go_to = [&](PagedWalk& at) {
@@ -458,15 +460,15 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     // Tile k of a unit sits kUnitCost + k behind the unit's start; there are at
     // most as many runs as there is cost, so no run inside a unit is without a
     // tile.
-    auto enter = [&](int c, PagedWalk& at, long long& t1) -> long long {
-      const long long t0 = runs.begin(c);
+    auto enter = [&](int c, PagedWalk& at, int& t1) -> int {
+      const int t0 = runs.begin(c);
       t1 = runs.begin(c + 1);
       // the last chunk that begins at or before t0 (those behind the last
       // sequence begin at the total)
       int lo = 0;
 #pragma unroll
-      for (int k = 0; k < FIND; k += 32) lo += __popc(__ballot_sync(0xffffffffu, (long long)sums[k + lane] * p.Hkv <= t0));
-      long long first = sums[lo - 1];
+      for (int k = 0; k < FIND; k += 32) lo += __popc(__ballot_sync(0xffffffffu, (int)(sums[k + lane] * p.Hkv) <= t0));
+      int first = (int)sums[lo - 1];
       at.b = min((lo - 1) * chunk, p.B - 1);
       go_to(at);
       while (t0 >= (first + at.tiles + kUnitCost) * p.Hkv && at.b < p.B - 1) {
@@ -476,14 +478,14 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
       }
       first *= p.Hkv;
       const int cost = at.tiles + kUnitCost;
-      at.kvh = (int)quot(t0 - first, cost);
-      const int off = (int)(t0 - first - (long long)at.kvh * cost);  // into the unit
+      at.kvh = (t0 - first) / cost;
+      const int off = t0 - first - at.kvh * cost;  // into the unit
       at.tile = max(0, off - kUnitCost);
       return t1 - t0 - max(0, kUnitCost - off);
     };
     PagedWalk at;
     int run = c;
-    long long left = 0, t1 = 0;  // cost of what is left of the run, from tile at.tile on; the run's end
+    int left = 0, t1 = 0;  // cost of what is left of the run, from tile at.tile on; the run's end
     if (whole) {
       if (c < units) {
         at.b = c / p.Hkv;
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     for (;;) {
       PagedCut run_cut{-1, 0, 0, 0};
       while (left > 0 && ok) {
-        const int n = (int)min((long long)(at.tiles - at.tile), left);
+        const int n = min(at.tiles - at.tile, left);
         const bool begins = at.tile == 0, ends = at.tile + n == at.tiles;
         const int* row = p.map.table + at.b * p.map.table_stride;
         // table entry of this lane's (tile, box) of the batch from tile k on

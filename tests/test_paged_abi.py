@@ -244,13 +244,11 @@ def _cut(B, Hkv, lens, start, grid, claim):
     def begin(c):
         if waves == 1:
             return c * total // runs
-        return (c // waves * 256 + share[c % waves]) * total // (256 * grid)
+        step = total // grid * 256 + total % grid * 256 // grid  # of a 256th of a stretch, in 65536ths
+        return total if c >= runs else (c // waves * 256 + share[c % waves]) * step >> 16
 
     def of(x):
-        if waves == 1:
-            return ((x + 1) * runs - 1) // total
-        n = ((x + 1) * 256 * grid - 1) // total
-        return n // 256 * waves + max(w for w in range(3) if w == 0 or share[w] <= n % 256)
+        return max(c for c in range(runs) if begin(c) <= x)
     assert begin(runs) == total
     if waves > 1:
         assert sorted(i % grid * waves + i // grid for i in range(runs)) == list(range(runs))
