@@ -505,31 +505,42 @@ def _same_device(first, *ts):
     return first.get_device()
 
 
+_torch = _current_device = _current_stream = None
+
+
+def _bind():
+    """torch's cheapest calls for the current device and stream (as numbers;
+    the public ones take 0.2 and 1.2 us), with the public ones where this
+    torch has no others."""
+    global _torch, _current_device, _current_stream
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+
+
 def _on(device, stream, call, *args):
     """``call(raw stream, *args)`` with ``device`` current, and on ``stream``
     if one is given, so that what is allocated inside belongs to the stream
     that the kernels run on."""
-    import torch
+    if _lib is None:
+        load_library()
+    if _torch is None:
+        _bind()
     if stream is None:
-        if torch.cuda.current_device() == device:
-            return call(_raw_stream(device), *args)
-        with torch.cuda.device(device):
-            return call(_raw_stream(device), *args)
+        if _current_device() == device:
+            return call(_current_stream(device), *args)
+        with _torch.cuda.device(device):
+            return call(_current_stream(device), *args)
+    cuda = _torch.cuda
     if not hasattr(stream, "cuda_stream"):
         raw = int(stream)
-        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+        stream = cuda.ExternalStream(raw, device=device) if raw else cuda.default_stream(device)
     if stream.device.index != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with cuda.device(device), cuda.stream(stream):
         return call(stream.cuda_stream, *args)
-
-
-def _raw_stream(device):
-    """The current stream of a device as a number (without the torch object
-    where this torch has the call: 1.2 us a time)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _int32(t, what, shape=None):
@@ -638,25 +649,25 @@ def _rope_layout(q, k, freqs, positions, cu_seqlens, outs):
 
 
 def _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, backward):
-    import torch
-    q_out, k_out = (None, None) if out is None else (out, None) if isinstance(out, torch.Tensor) else out
-    if out is not None and (q_out is None or (k is None) != (k_out is None)):
-        raise ValueError("out must give a tensor for each input")
+    if out is None:
+        q_out = k_out = None
+    else:
+        q_out, k_out = out if isinstance(out, (tuple, list)) else (out, None)
+        if q_out is None or (k is None) != (k_out is None):
+            raise ValueError("out must give a tensor for each input")
     known = _known(("rope", _sig(q), _sig(k), _sig(freqs), _sig(positions), _sig(cu_seqlens), _sig(q_out), _sig(k_out)),
                    _rope_layout, q, k, freqs, positions, cu_seqlens, (q_out, k_out))
-    load_library()
     return _on(known[0], stream, _rope_call, known, q, k, freqs, positions, cu_seqlens, interleaved, amp, q_out, k_out,
                backward)
 
 
 def _rope_call(raw, known, q, k, freqs, positions, cu_seqlens, interleaved, amp, yq, yk, backward):
-    import torch
     _, dt, rot, B, S, D, nseq, pos_stride, rows, empty = known
     given = yq is not None
     if not given:
-        yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        yq = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k is not None:
-            yk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            yk = _torch.empty(k.shape, dtype=k.dtype, device=k.device)
     xp, yp = q.data_ptr(), yq.data_ptr()
     x, y = _ROWS.pack(xp, *rows[0][0]), _ROWS.pack(yp, *rows[0][1])
     if given:
@@ -771,19 +782,17 @@ def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
         ("append", _sig(k), _sig(v), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), _sig(cu_seqlens),
          _sig(q), _sig(freqs), _sig(positions), _sig(q_out)),
         _append_layout, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions, q_out)
-    load_library()
     return _on(known[0], stream, _append_call, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q,
                freqs, positions, interleaved, amp, q_out)
 
 
 def _append_call(raw, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q, freqs, positions,
                  interleaved, amp, q_out):
-    import torch
     _, dt, B, T, D, pages, k_rows, v_rows, q_rows, rot = known
     to, qx, qy = q_out, None, None
     if q is not None:
         if q_out is None:
-            to = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            to = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
         xp, yp = q.data_ptr(), to.data_ptr()
         if q_out is not None:
             _apart(xp, yp, q_rows)
@@ -831,22 +840,20 @@ def _decode_pages(q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix
         ("decode", _sig(q), _sig(k_pages), _sig(v_pages), _sig(block_table), _sig(seq_lens), prefix_len,
          _sig(prefix_table), _sig(out), _sig(lse), _sig(workspace)),
         _decode_layout, q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, out, lse, workspace)
-    load_library()
     return _on(known[0], stream, _decode_call, known, q, k_pages, v_pages, block_table, seq_lens, prefix_len,
                prefix_table, scale, out, lse, workspace)
 
 
 def _decode_call(raw, known, q, k_pages, v_pages, block_table, seq_lens, prefix_len, prefix_table, scale, o, lse, ws):
-    import torch
     _, dt, B, Hq, D, pages, need, size = known
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if o is None:
-        o = torch.empty_like(q)
+        o = _torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        lse = _torch.empty((B, Hq), device=q.device, dtype=_torch.float32)
     if ws is None:
-        ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+        ws = _torch.empty(max(need, 1), device=q.device, dtype=_torch.uint8)
     at = _pack_pages(k_pages, v_pages, block_table, pages)
     if prefix_len:
         st = _lib.fa_decode_prefix(q.data_ptr(), at, seq_lens.data_ptr(), prefix_len, _ptr(prefix_table), o.data_ptr(),
