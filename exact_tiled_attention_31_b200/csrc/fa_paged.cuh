@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
     const long long i = (long long)c * C::THREADS + threadIdx.x;
     if (i * 64 < (long long)p.B * p.Hq * D) prefetch_l2(p.q + i * 64);
     if (i * 32 < p.B) prefetch_l2(p.seq_lens + i * 32);
-    if (i < p.B) prefetch_l2(p.map.table + i * p.map.table_stride + (p.start >> p.map.page_shift));
+    if (i < p.B && p.start < p.map.max_len)
+      prefetch_l2(p.map.table + i * p.map.table_stride + (p.start >> p.map.page_shift));
   }
   // Behind prefix_kernel (which has itself waited for all before it) this kernel
   // runs ahead: it reads nothing of that one's, and only waits for its end.

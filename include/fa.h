@@ -445,7 +445,13 @@ fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, 
  * Pages may hold anything (NaN too) in rows at or past len_b.  A page outside
  * [0, n_pages) counts as zeros and fa_check_device_error() then returns
  * FA_ERR_INVALID_ARG.  Hq a multiple of Hkv, G <= 16.  The work is cut by the
- * lengths on the device, so one recorded graph serves all lengths.
+ * lengths on the device, so one recorded graph serves all lengths; which SM
+ * takes what does not change the result, so equal calls on one GPU give equal
+ * bits.  The workspace may be reused once the call's work on `stream` has
+ * finished; calls that run at the same time need one each.  Heads * (rows / 64
+ * + 3), summed over the sequences, may be at most 2^31 (checked on the device:
+ * nothing is written and fa_check_device_error() returns FA_ERR_INVALID_ARG).
+ * One to three kernel launches on `stream`.
  */
 /* The two-phase size query ("ops-transformer里的完整算子"); the size is for the
  * current device (one part per SM boundary).  0 for unsupported arguments. */
@@ -463,7 +469,7 @@ fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_l
  * block_table and seq_lens are those of fa_decode_paged: rows from prefix_len
  * on are found in each sequence's own row of the table, and a sequence shorter
  * than prefix_len sees the first len_b shared rows.  Every shared row must
- * hold finite values.
+ * hold finite values.  Three or four kernel launches on `stream`.
  */
 /* The two-phase size query ("ops-transformer里的完整算子"), for the current device. */
 size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int D);

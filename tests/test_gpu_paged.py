@@ -329,3 +329,21 @@ def test_prompts_then_steps(cuda_device, dtype, page, shared):
             ref = op.decode_paged(yq[b:b + 1].cpu(), hist_k[b][None], hist_v[b][None], ONE_PAGE, [now[b]], scale)
             check_decode(o[b:b + 1], lse[b:b + 1], yq[b:b + 1], ref, f"step {step} sequence {b}")
 
+
+
+@pytest.mark.parametrize("dtype,mult", [("bf16", 8.0), ("fp16", 8.0), ("bf16", 64.0)])
+def test_prefix_of_large_and_growing_scores(cuda_device, dtype, mult):
+    """Scores of hundreds whose maximum grows along the shared rows, in small steps
+    and large ones: the lagging maximum and every rescaling of O."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(17)
+    B, Hq, Hkv, D, page, P = 12, 8, 1, 64, 64, 1344
+    lens = [P + 9 * i for i in range(B)]
+    kp, vp, table = make_cache(gen, lens, Hkv, D, page, dtype, shared=P // page)
+    q = randn(gen, dtype, B, Hq, D)
+    grow = torch.linspace(0.02, 1.0, P // page) ** 2 * mult
+    for i in range(P // page):
+        kp[table[0, i]] *= grow[i]
+    args = (q.to(dev), kp.to(dev), vp.to(dev), table.to(dev), _i32(lens, dev))
+    o, lse = fa.decode_prefix(*args, P, scale=0.125)
+    fa.check_device_error()
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, 0.125), f"growing scores {dtype} x {mult}")
