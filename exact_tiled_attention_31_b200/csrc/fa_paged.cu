@@ -112,6 +112,17 @@ int prefix_splits(long long units, int P) {
   return (int)best;
 }
 
+// Whether shared rows are worth a pass of their own.  Below 24 MB read once more
+// than needed (from L2 mostly), or with up to three sequences, paged_kernel
+// alone, reading them for each sequence, is done before prefix_kernel and the
+// join are: 4 sequences x 1024 rows x 8 heads of 128, 13 MB more: 11.5 against
+// 11.1 us on the GPU, but two launches instead of three (11.5 against 13.9 us
+// for the call); 32 x 1024, 130 MB: 20.5 against 16.0; 2 x 16384, 67 MB: 18.8
+// against 27.1; 4 x 16384: 27.8 against 27.6.
+bool shared_pass(int B, int Hkv, int P, int D) {
+  return P > 0 && B > 3 && (double)(B - 1) * P * Hkv * D * 4 > 24e6;
+}
+
 struct PagedWs {
   size_t next_run, cuts, lse_part, o_part, pre_lse, pre_o, own_lse, own_o, total;
   int n_pre, n_pairs, per_tile;
@@ -124,7 +135,7 @@ PagedWs paged_layout(int B, int Hq, int Hkv, int P, int D) {
   PagedWs w;
   w.per_tile = 128 / G;
   w.n_pairs = (int)(((long long)B + 2 * w.per_tile - 1) / (2 * w.per_tile));
-  w.n_pre = P > 0 ? prefix_splits((long long)Hkv * w.n_pairs, P) : 0;
+  w.n_pre = shared_pass(B, Hkv, P, D) ? prefix_splits((long long)Hkv * w.n_pairs, P) : 0;
   const size_t pre = (size_t)w.n_pre * B * Hq, own = w.n_pre ? (size_t)B * Hq : 0;
   w.next_run = 0;
   w.cuts = 256;
@@ -262,7 +273,9 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   fa::PagedParams p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.seq_lens = seq_lens;
-  p.map = {pages->block_table, pages->table_stride, pages->n_pages, log2_of(pages->page_size), max_len};
+  const int* shared = prefix_table ? prefix_table : pages->block_table;  // the first sequence's row
+  p.map = {pages->block_table, pages->table_stride, pages->n_pages, log2_of(pages->page_size), max_len, shared,
+           prefix_len};
   p.o_part = reinterpret_cast<float*>(ws + w.o_part);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
   p.cuts = reinterpret_cast<fa::PagedCut*>(ws + w.cuts);
@@ -273,13 +286,13 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   p.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
   p.own_o = reinterpret_cast<float*>(ws + w.own_o);
   p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
-  p.n_pre = w.n_pre, p.start = prefix_len;
+  p.n_pre = w.n_pre, p.start = w.n_pre ? prefix_len : 0;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
   fa::PrefixParams pre = {};
   pre.seq_lens = seq_lens;
   pre.map = p.map;
-  if (prefix_table) pre.map.table = prefix_table;  // else the first sequence's row
+  pre.map.table = shared;
   pre.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
   pre.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
   pre.P = prefix_len, pre.n_pre = w.n_pre, pre.n_pairs = w.n_pairs, pre.per_tile = w.per_tile;

@@ -39,6 +39,8 @@ struct PagedMap {       // how rows of a sequence are found
   const int* table;     // [B, max_pages] by table_stride
   long long table_stride;
   int n_pages, page_shift, max_len;  // max_len: rows the table holds
+  const int* shared;    // the pages of the first n_shared rows of every sequence
+  int n_shared;
 };
 
 // A cut unit: its first and last run.
@@ -526,7 +528,9 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
         auto find = [&](int k) {
           const int i = k + lane / boxes;
           const int first = p.start + (at.tile + i) * C::KT + (lane % boxes) * box;
-          return i < n && lane < batch * boxes && first < at.end ? row[first >> p.map.page_shift] : -1;
+          return i < n && lane < batch * boxes && first < at.end
+                     ? (first < p.map.n_shared ? p.map.shared : row)[first >> p.map.page_shift]
+                     : -1;
         };
         int ids = find(0);
         for (int k = 0; k < n && ok; k += batch) {

@@ -469,7 +469,9 @@ fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_l
  * block_table and seq_lens are those of fa_decode_paged: rows from prefix_len
  * on are found in each sequence's own row of the table, and a sequence shorter
  * than prefix_len sees the first len_b shared rows.  Every shared row must
- * hold finite values.  Three or four kernel launches on `stream`.
+ * hold finite values.  Where reading the shared rows for each sequence is
+ * sooner done (up to three sequences, or 24 MB more to read), that is what the
+ * call does.  One to four kernel launches on `stream`.
  */
 /* The two-phase size query ("ops-transformer里的完整算子"), for the current device. */
 size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int D);

@@ -240,13 +240,17 @@ def test_decode_reports_a_bad_page(cuda_device):
 # ---------------------------------------------------------------- shared prefix
 
 @pytest.mark.parametrize("B,Hq,Hkv,D,page,P,own,dtype", [
+    # read for each sequence (up to 24 MB more to read)
     (1, 4, 4, 64, 16, 16, [5], "bf16"),
     (3, 8, 2, 128, 64, 128, [0, 1, 200], "bf16"),
-    (5, 5, 1, 64, 16, 272, [7, 0, 64, 65, 33], "fp16"),           # group 5: 25 sequences a tile
-    (40, 16, 1, 128, 32, 416, [i for i in range(40)], "fp16"),     # 640 rows: three pairs of tiles
+    (5, 5, 1, 64, 16, 272, [7, 0, 64, 65, 33], "fp16"),
+    # a pass of their own
+    (91, 5, 1, 64, 16, 1072, [i % 71 for i in range(91)], "fp16"),   # group 5: 25 sequences a tile
+    (40, 16, 1, 128, 32, 1248, [i for i in range(40)], "fp16"),      # 640 rows: three pairs of tiles
     (70, 4, 2, 128, 256, 512, [3 * i for i in range(70)], "bf16"),
-    (140, 2, 2, 64, 16, 1040, [1] * 140, "bf16"),                  # one row a sequence, two tiles
-    (6, 9, 1, 128, 16, 1600, [0] * 6, "bf16"),                     # nothing of their own; group 9
+    (140, 2, 2, 64, 16, 1040, [1] * 140, "bf16"),                    # one row a sequence, two tiles
+    (4, 1, 1, 128, 64, 16384, [9, 0, 64, 300], "bf16"),              # four query rows, cut over all SMs
+    (32, 9, 1, 128, 16, 1600, [0] * 32, "bf16"),                     # nothing of their own; group 9
 ])
 def test_prefix_matches_oracle(cuda_device, B, Hq, Hkv, D, page, P, own, dtype):
     args, o, lse = _decode_case(cuda_device, [P + n for n in own], Hq, Hkv, D, page, dtype, seed=P + B, shared=P)
@@ -256,11 +260,12 @@ def test_prefix_matches_oracle(cuda_device, B, Hq, Hkv, D, page, P, own, dtype):
     assert (pl - lse).abs().max() <= 1e-4
 
 
-def test_prefix_of_short_and_empty_sequences(cuda_device):
+@pytest.mark.parametrize("many", [1, 9])  # read for each sequence; a pass of their own
+def test_prefix_of_short_and_empty_sequences(cuda_device, many):
     """Lengths below the shared part: padding rows and sequences that see part of it."""
     dev, gen = cuda_device, torch.Generator().manual_seed(5)
     P, page, Hq, Hkv, D = 320, 32, 8, 2, 128
-    lens = [0, 1, 31, 64, 129, 319, 320, 321, 400]
+    lens = [0, 1, 31, 64, 129, 319, 320, 321, 400] * many
     kp, vp, table = make_cache(gen, lens, Hkv, D, page, "bf16", shared=P // page)
     q = randn(gen, "bf16", len(lens), Hq, D)
     prefix = table[0, :P // page].clone()
@@ -336,8 +341,8 @@ def test_prefix_of_large_and_growing_scores(cuda_device, dtype, mult):
     """Scores of hundreds whose maximum grows along the shared rows, in small steps
     and large ones: the lagging maximum and every rescaling of O."""
     dev, gen = cuda_device, torch.Generator().manual_seed(17)
-    B, Hq, Hkv, D, page, P = 12, 8, 1, 64, 64, 1344
-    lens = [P + 9 * i for i in range(B)]
+    B, Hq, Hkv, D, page, P = 80, 8, 1, 64, 64, 1344
+    lens = [P + 2 * i for i in range(B)]
     kp, vp, table = make_cache(gen, lens, Hkv, D, page, dtype, shared=P // page)
     q = randn(gen, dtype, B, Hq, D)
     grow = torch.linspace(0.02, 1.0, P // page) ** 2 * mult

@@ -71,7 +71,8 @@ def _capture(fn):
     return g
 
 
-@pytest.mark.parametrize("shared", [0, 128])
+# (shared rows: none; read for each sequence; a pass of their own)
+@pytest.mark.parametrize("shared", [0, 128, 6528])
 def test_one_graph_serves_all_lengths(cuda_device, shared):
     """A recorded step replayed with other inputs and lengths, padding rows among them."""
     s = Step(cuda_device, shared=shared)
@@ -130,10 +131,10 @@ def test_graph_of_rotation_and_attention(cuda_device):
 
 
 @pytest.mark.parametrize("dirty", [0x00, 0x7F, 0xFF])
-@pytest.mark.parametrize("shared", [0, 64])
+@pytest.mark.parametrize("shared", [0, 64, 9024])
 def test_any_workspace_contents(cuda_device, dirty, shared):
-    s = Step(cuda_device, B=3, shared=shared, dirty=dirty, room=2000)
-    s.set([shared + n for n in (1999, 3, 700)], 7)
+    s = Step(cuda_device, B=4, shared=shared, dirty=dirty, room=2000)
+    s.set([shared + n for n in (1999, 3, 700, 0)], 7)
     s()
     s.check(f"workspace of {dirty:#x}")
 
@@ -164,9 +165,9 @@ def test_other_streams(cuda_device):
 
 def test_two_calls_at_once(cuda_device):
     """Two long calls on two streams, each with its own workspace, give what each gives alone."""
-    a, b = Step(cuda_device, B=6, room=6000, seed=1), Step(cuda_device, B=6, room=6000, seed=2, shared=512)
+    a, b = Step(cuda_device, B=6, room=6000, seed=1), Step(cuda_device, B=6, room=6000, seed=2, shared=5120)
     a.set([6000, 5999, 1, 0, 3333, 64], 1)
-    b.set([512 + n for n in (6000, 17, 2000, 0, 64, 5000)], 2)
+    b.set([5120 + n for n in (6000, 17, 2000, 0, 64, 5000)], 2)
     a(), b()
     torch.cuda.synchronize()
     want = [x.clone() for x in (a.o, a.lse, b.o, b.lse)]
@@ -180,7 +181,7 @@ def test_two_calls_at_once(cuda_device):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,D,page,shared", [(8, 16, 8, 64, 64, 0), (150, 8, 2, 64, 16, 0), (9, 16, 8, 64, 32, 64),
+@pytest.mark.parametrize("B,Hq,Hkv,D,page,shared", [(8, 16, 8, 64, 64, 0), (150, 8, 2, 64, 16, 0), (9, 16, 8, 64, 32, 1536),
                                                     (12, 32, 2, 128, 128, 0)])
 def test_handed_out_runs(cuda_device, B, Hq, Hkv, D, page, shared):
     """Enough rows that the CTAs take short runs from the common count: every
@@ -245,7 +246,7 @@ def test_pool_beyond_32_bits(cuda_device):
 
 def test_nan_stays_in_its_row(cuda_device):
     """A query or a visible key that is NaN gives NaN in the rows that see it, and in no others."""
-    for shared in (0, 64):
+    for shared in (0, 64, 8192):
         s = Step(cuda_device, B=4, shared=shared)
         s.set([shared + 40] * 4, 3)
         s()

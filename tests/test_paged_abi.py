@@ -129,7 +129,10 @@ def test_append_refusals():
 def test_decode_refusals_and_workspace():
     size = fa.fa_decode_paged_workspace_size(4, 8, 2, 128)
     pre = fa.fa_decode_prefix_workspace_size(4, 8, 2, 640, 128)
-    assert 0 < size < pre and fa.fa_decode_prefix_workspace_size(4, 8, 2, 0, 128) == size
+    assert 0 < size == pre == fa.fa_decode_prefix_workspace_size(4, 8, 2, 0, 128)  # read for each sequence
+    # a pass of its own takes fp32 parts of every row besides
+    more = fa.fa_decode_prefix_workspace_size(64, 8, 2, 640, 128) - fa.fa_decode_paged_workspace_size(64, 8, 2, 128)
+    assert more >= 2 * 64 * 8 * (128 + 1) * 4
     for bad in ((0, 8, 2, 128), (4, 0, 2, 128), (4, 8, 0, 128), (4, 9, 2, 128), (4, 34, 2, 128), (4, 8, 2, 96)):
         assert fa.fa_decode_paged_workspace_size(*bad) == 0, bad
     assert fa.fa_decode_prefix_workspace_size(4, 8, 2, -64, 128) == 0
