@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(768, 1)
       mbar_init(&stats_ready[i], 256);
       mbar_init(&o_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 256);  // both halves of a tile
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -233,37 +233,33 @@ __global__ void __launch_bounds__(768, 1)
         mma_commit_e(&s_full[t], e);
       }
       if (ok) mma_commit_e(&kv_empty[ks], e);
+      // Everything that is ready early is waited for before P, so that P V and
+      // the next Q K^T of a tile go out back to back: every wait here is ahead of
+      // the tile's next scores (each takes 150 to 200 cycles even when it has
+      // nothing to wait for: four of them behind P were 1700 of a step's 3950).
       for (int j = 0; j < n_kv && ok; ++j) {
         uint32_t vs;
         take(vs);
+        if (j + 1 < n_kv) take(ks);
         if (!ok) break;
-        bool have_k = false;
         for (int t = 0; t < 2; ++t) {
-          const int n_t = t ? n1 : n0;
-          if (j >= n_t) continue;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[2 * t], j & 1, FWD_SITE_P)))) break;
+          if (j >= (t ? n1 : n0)) continue;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_ready[t], j & 1, FWD_SITE_OR)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[t], j & 1, FWD_SITE_P)))) break;
           tc_fence_after();
           pv(t, 0, vs, j > 0 ? 1u : 0u);
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[2 * t + 1], j & 1, FWD_SITE_P)))) break;
-          tc_fence_after();
           pv(t, 1, vs, 1u);
           mma_commit_e(&pv_done[t], e);
-          if (j == n_t - 1) {
+          if (j == n_kv - 1) {
             mma_commit_e(&o_full[t], e);
           } else {
-            if (!have_k) {
-              take(ks);
-              if (!ok) break;
-              have_k = true;
-            }
             qk(t, ks);
             mma_commit_e(&s_full[t], e);
           }
         }
         if (!ok) break;
         mma_commit_e(&kv_empty[vs], e);
-        if (have_k) mma_commit_e(&kv_empty[ks], e);
+        if (j + 1 < n_kv) mma_commit_e(&kv_empty[ks], e);
       }
       mma_commit_e(drain, e);
       mbar_wait(drain, 0, FWD_SITE_DRAIN);
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(768, 1)
       tmem_st32(tS + 32 * h, pk);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&p_full[2 * t + h]);
+      mbar_arrive(&p_full[t]);
       float f0, f1, f2_, f3, r0, r1, r2, r3;
       f2split(fsum0, f0, f1);
       f2split(fsum1, f2_, f3);
