@@ -64,13 +64,13 @@ fa_status launch_after(void (*kern)(A...), dim3 grid, int block, uint32_t smem, 
 }
 
 // ---------------------------------------------------------------- rotary positions
-// Blocks of `rows` tokens of `heads` heads, the heads' index first where the
-// heads of a token are nearer than its neighbours (and the tokens' fits second).
+// Blocks of `rows` tokens and `groups` groups of heads, the group's index first
+// where the heads of a token are nearer than its neighbours (and the tokens'
+// fits second).
 template <int D>
-dim3 rope_grid(long long rows, int heads, long long head_stride, long long row_stride, bool& heads_near) {
+dim3 rope_grid(long long rows, int groups, long long head_stride, long long row_stride, bool& heads_near) {
   constexpr int TOKENS = fa::kRopeThreads / (D / 16);
   const unsigned tiles = (unsigned)((rows + TOKENS - 1) / TOKENS);
-  const unsigned groups = (heads + fa::kRopeHeads - 1) / fa::kRopeHeads;
   heads_near = head_stride < row_stride && tiles <= 65535;
   return heads_near ? dim3(groups, tiles) : dim3(tiles, groups);
 }
@@ -78,14 +78,14 @@ dim3 rope_grid(long long rows, int heads, long long head_stride, long long row_s
 template <int D, bool BF16>
 fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
   if ((long long)p.B * p.S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  const dim3 grid = rope_grid<D>((long long)p.B * p.S, p.heads[0] + p.heads[1], p.x[0].head, p.x[0].row, p.heads_near);
+  const dim3 grid = rope_grid<D>((long long)p.B * p.S, fa::rope_groups(p.heads[0]) + fa::rope_groups(p.heads[1]), p.x[0].head, p.x[0].row, p.heads_near);
   return launch_after(inter ? fa::rope_kernel<D, BF16, true> : fa::rope_kernel<D, BF16, false>, grid, fa::kRopeThreads,
                       0, st, p);
 }
 
 template <int D, bool BF16>
 fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
-  const dim3 grid = rope_grid<D>(p.T, p.Hq + 2 * p.Hkv, p.k.head, p.k.row, p.heads_near);
+  const dim3 grid = rope_grid<D>(p.T, fa::rope_groups(p.Hq) + 2 * fa::rope_groups(p.Hkv), p.k.head, p.k.row, p.heads_near);
   return launch_after(inter ? fa::append_kernel<D, BF16, true> : fa::append_kernel<D, BF16, false>, grid,
                       fa::kRopeThreads, 0, st, p);
 }

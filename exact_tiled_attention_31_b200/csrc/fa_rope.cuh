@@ -58,8 +58,9 @@ __device__ __forceinline__ int seq_of(const int* cu, int nseq, int t) {
   return lo < nseq ? lo : -1;
 }
 
-__device__ __forceinline__ void rope_angle(double freq, int pos, float amp, float& c, float& s) {
-  double turns = (double)pos * (freq * 0.15915494309189533577);
+// cosine and sine of pair `freq` at a position of `cycles` = position / 2 pi
+__device__ __forceinline__ void rope_angle(double freq, double cycles, float amp, float& c, float& s) {
+  double turns = cycles * freq;
   turns -= rint(turns);
   const float x = (float)turns * 6.2831853071795865f;
   c = __cosf(x) * amp;
@@ -103,6 +104,42 @@ __device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float (&c)[8
   }
 }
 
+// n <= kRopeHeads rows of one token, xs and ys elements apart: turned by `pos`
+// (with sign -1 back) if `turn`, else copied.
+template <int D, bool BF16, bool INTER>
+__device__ __forceinline__ void rope_heads(const RopeItem<D, INTER>& item, const uint16_t* x, long long xs, uint16_t* y,
+                                           long long ys, int n, bool turn, const double* freqs, int pos, float amp,
+                                           float sign) {
+  uint4 lo[kRopeHeads], hi[kRopeHeads];
+#pragma unroll
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (k < n) {
+      lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
+      hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
+      x += xs;
+    }
+  turn = turn && item.turn;
+  float c[8], s[8];
+  if (turn) {
+    const double cycles = (double)pos * 0.15915494309189533577;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      rope_angle(freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], cycles, amp, c[j], s[j]);
+      s[j] *= sign;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRopeHeads; ++k)
+    if (k < n) {
+      if (turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+      *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
+      *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
+      y += ys;
+    }
+}
+// groups of kRopeHeads heads, none of them over two tensors
+__host__ __device__ constexpr int rope_groups(int heads) { return (heads + kRopeHeads - 1) / kRopeHeads; }
+
 struct RopeParams {
   RowsIn x[2];
   RowsOut y[2];
@@ -135,41 +172,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     pos = t - p.cu[s];
   }
   if (p.positions) pos = p.positions[b * p.pos_batch + t];
-  const RopeItem<D, INTER> item(it, p.R);
-  const int h0 = group * kRopeHeads, h1 = min(h0 + kRopeHeads, p.heads[0] + p.heads[1]);
-  // head h of both tensors' heads in one row: h < heads[0] is the first's
-  auto in = [&](int h) {
-    const int w = h >= p.heads[0];
-    return p.x[w].p + b * p.x[w].batch + (long long)(h - (w ? p.heads[0] : 0)) * p.x[w].head + t * p.x[w].row;
-  };
-  auto out = [&](int h) {
-    const int w = h >= p.heads[0];
-    return p.y[w].p + b * p.y[w].batch + (long long)(h - (w ? p.heads[0] : 0)) * p.y[w].head + t * p.y[w].row;
-  };
-  uint4 lo[kRopeHeads], hi[kRopeHeads];
-#pragma unroll
-  for (int k = 0; k < kRopeHeads; ++k)
-    if (h0 + k < h1) {
-      const uint16_t* x = in(h0 + k);
-      lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
-      hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
-    }
-  float c[8], s[8];
-  if (item.turn) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
-      s[j] *= p.sign;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kRopeHeads; ++k)
-    if (h0 + k < h1) {
-      if (item.turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
-      uint16_t* y = out(h0 + k);
-      *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
-      *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
-    }
+  const int first = rope_groups(p.heads[0]);
+  const bool w = group >= first;  // which tensor
+  const int h = (group - (w ? first : 0)) * kRopeHeads;
+  const RowsIn x = w ? p.x[1] : p.x[0];
+  const RowsOut y = w ? p.y[1] : p.y[0];
+  rope_heads<D, BF16, INTER>(RopeItem<D, INTER>(it, p.R), x.p + b * x.batch + h * x.head + t * x.row, x.head,
+                             y.p + b * y.batch + h * y.head + t * y.row, y.head, (w ? p.heads[1] : p.heads[0]) - h, true,
+                             p.freqs, pos, p.amp, p.sign);
 }
 
 // ---------------------------------------------------------------------------
@@ -228,46 +238,22 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   const int page = slot < p.max_pages ? p.table[b * p.table_stride + slot] : -1;
   const bool placed = page >= 0 && page < p.n_pages;
   if (!placed && it == 0 && group == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
-  const long long at = placed ? page * p.page_stride + (long long)row * D : 0;
+  // q's groups of heads, then k's, then v's
   const RopeItem<D, INTER> item(it, p.R);
-  // heads in one row: q's Hq, k's Hkv, v's Hkv
-  const int hk = p.Hq, hv = p.Hq + p.Hkv;
-  const int h0 = group * kRopeHeads, h1 = min(h0 + kRopeHeads, hv + p.Hkv);
-  auto in = [&](int h) {
-    return h < hk   ? p.q.p + h * p.q.head + t * p.q.row
-           : h < hv ? p.k.p + (h - hk) * p.k.head + t * p.k.row
-                    : p.v.p + (h - hv) * p.v.head + t * p.v.row;
-  };
-  auto out = [&](int h) -> uint16_t* {
-    if (h < hk) return p.q_out.p + h * p.q_out.head + t * p.q_out.row;
-    if (!placed) return nullptr;
-    const long long off = at + ((long long)(h < hv ? h - hk : h - hv) << p.page_shift) * D;
-    return (h < hv ? p.k_pages : p.v_pages) + off;
-  };
-  uint4 lo[kRopeHeads], hi[kRopeHeads];
-#pragma unroll
-  for (int k = 0; k < kRopeHeads; ++k)
-    if (h0 + k < h1) {
-      const uint16_t* x = in(h0 + k);
-      lo[k] = *reinterpret_cast<const uint4*>(x + item.lo);
-      hi[k] = *reinterpret_cast<const uint4*>(x + item.hi);
-    }
-  float c[8], s[8];
-  if (item.turn && h0 < hv) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      rope_angle(p.freqs[(j < 4 ? item.f_lo : item.f_hi) + (j & 3)], pos, p.amp, c[j], s[j]);
+  const int gq = rope_groups(p.Hq), gk = gq + rope_groups(p.Hkv);
+  if (group < gq) {
+    const int h = group * kRopeHeads;
+    rope_heads<D, BF16, INTER>(item, p.q.p + h * p.q.head + t * p.q.row, p.q.head,
+                               p.q_out.p + h * p.q_out.head + t * p.q_out.row, p.q_out.head, p.Hq - h, true, p.freqs,
+                               pos, p.amp, 1.f);
+  } else if (placed) {
+    const bool val = group >= gk;
+    const int h = (group - (val ? gk : gq)) * kRopeHeads;
+    const RowsIn x = val ? p.v : p.k;
+    uint16_t* y = (val ? p.v_pages : p.k_pages) + page * p.page_stride + ((((long long)h << p.page_shift) + row) * D);
+    rope_heads<D, BF16, INTER>(item, x.p + h * x.head + t * x.row, x.head, y, (long long)D << p.page_shift, p.Hkv - h,
+                               !val, p.freqs, pos, p.amp, 1.f);
   }
-#pragma unroll
-  for (int k = 0; k < kRopeHeads; ++k)
-    if (h0 + k < h1) {
-      if (item.turn && h0 + k < hv) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
-      uint16_t* y = out(h0 + k);
-      if (y) {
-        *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
-        *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
-      }
-    }
 }
 
 }  // namespace fa
