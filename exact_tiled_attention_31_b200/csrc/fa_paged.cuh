@@ -32,6 +32,7 @@
 #pragma once
 
 #include "fa_decode.cuh"
+#include "pdl.cuh"
 
 namespace fa {
 

@@ -29,6 +29,7 @@
 // other that costs 1 %: 81.0 against 80.2 us for 64 heads x 8192 twice).
 #pragma once
 
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace fa {

@@ -18,9 +18,10 @@ namespace fa {
 // ---------------------------------------------------------------------------
 enum : uint32_t { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_ARG = 2 };
 
-// One pair per translation unit; fa_check_device_error() looks at each.
-static __device__ uint32_t g_dev_error = 0;   // first error code (0 = none)
-static __device__ uint32_t g_dev_where = 0;   // site id of the first error
+// Each translation unit of the library has its own pair (device variables are
+// local to theirs); fa_check_device_error() looks at both.
+__device__ uint32_t g_dev_error = 0;   // first error code (0 = none)
+__device__ uint32_t g_dev_where = 0;   // site id of the first error
 
 // Upper bound on any single barrier wait.  Every wait in a healthy launch
 // lasts microseconds; this bound only turns a logic error into a clean exit.
@@ -420,14 +421,6 @@ template <uint32_t N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-
-// Programmatic dependent launch.  A kernel launched with that attribute may
-// begin before the one ahead of it on the stream ends: pdl_wait() returns once
-// everything ahead has completed and its writes are visible.  pdl_launch()
-// lets the kernel behind begin in the same way; after pdl_wait() what is ahead
-// of this kernel is then complete for that one before it waits itself.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Named barrier over `count` threads (a multiple of 32).
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t count) {
