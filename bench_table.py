@@ -1,16 +1,17 @@
 #!/usr/bin/env python
 """Timing table of the attention kernels over the shapes beside the headline
 workload: dense forward/backward (atomic and deterministic dQ), dropout,
-packed variable-length batches and decode.  One JSON line per row.
+packed variable-length batches, decode, and decode over a paged cache with the
+rotation and append around it.  One JSON line per row.
 
-    python bench_table.py [--only dense,dropout,varlen,decode] [--iters N]
+    python bench_table.py [--only dense,dropout,varlen,decode,paged] [--iters N]
 
 Device time with CUDA events on the launching stream, at least 3 warm-up
 calls, the mean of ``--iters`` calls, queued behind a ~10 ms spin so that the
 host's launch overhead never shows in a short call's events.  The forward/backward rows write a
 256 MiB buffer (above the 126 MB L2) between calls, outside the event pairs;
-the decode rows alternate two input sets instead (each set's caches exceed
-L2).  FLOPs follow bench.py's convention (forward 4*S^2*D per head, halved
+the decode and paged rows alternate two input sets instead (each set's caches
+exceed L2).  FLOPs follow bench.py's convention (forward 4*S^2*D per head, halved
 under a causal mask; backward 2.5x that); decode counts the K and V cache
 bytes read once.
 """
@@ -56,7 +57,7 @@ def flop_count(lengths, heads: int, d: int, causal: bool):
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--only", default="dense,dropout,varlen,decode")
+    ap.add_argument("--only", default="dense,dropout,varlen,decode,paged")
     ap.add_argument("--iters", type=int, default=20)
     args = ap.parse_args()
     parts = set(args.only.split(","))
@@ -153,8 +154,9 @@ def main():
             emit({"kind": "varlen", "shape": f"{name}: T={t['total']} H{H} D{D} lengths {lo}..{hi}", "dtype": "bf16",
                   "causal": True, "fwd_us": t_f * 1e3, "bwd_us": t_b * 1e3, "fwd_tflops": f_f / t_f / 1e9,
                   "bwd_tflops": f_b / t_b / 1e9, "fwd_bwd_tflops": (f_f + f_b) / (t_f + t_b) / 1e9})
-    if "decode" in parts:
+    if "decode" in parts or "paged" in parts:
         del flush
+    if "decode" in parts:
         for B, Hq, Hkv, L, D in DECODE:
             sets = []
             for seed in (42, 43):
@@ -174,6 +176,54 @@ def main():
                 t_d = timed(dec, max(args.iters, 30), do_flush=False)
                 emit({"kind": "decode", "shape": f"B{B} Hq{Hq} Hkv{Hkv} L{L} D{D}", "dtype": "bf16",
                       "n_splits": n if n else "balanced (0)", "us": t_d * 1e3, "gbs": nbytes / t_d / 1e6})
+    if "paged" in parts:
+        page = 64
+        for B, Hq, Hkv, L, D in DECODE:
+            gen = torch.Generator(device=dev).manual_seed(42)
+            n = L // page
+            sets = []
+            for _ in range(2):
+                pools = [torch.randn(B * n, Hkv, page, D, device=dev, generator=gen).to(torch.bfloat16)
+                         for _ in range(2)]
+                table = torch.randperm(B * n, device=dev, generator=gen).to(torch.int32).view(B, n)
+                qkv = [torch.randn(B, h, D, device=dev, generator=gen).to(torch.bfloat16) for h in (Hq, Hkv, Hkv)]
+                sets.append((*pools, table, *qkv))
+            freqs, amp = fa.rope_freqs(D, device=dev)
+            lens = torch.full((B,), L, dtype=torch.int32, device=dev)
+            rq, o = torch.empty_like(sets[0][3]), torch.empty_like(sets[0][3])
+            lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
+            ws = torch.empty(fa.fa_decode_paged_workspace_size(B, Hq, Hkv, D), device=dev, dtype=torch.uint8)
+
+            def app(i):
+                kp, vp, table, q, k, v = sets[i % 2]
+                fa.append_paged(k, v, kp, vp, table, lens, q=q, freqs=freqs, amp=amp, q_out=rq)
+
+            def dec(i):
+                kp, vp, table, *_ = sets[i % 2]
+                fa.decode_paged(rq, kp, vp, table, lens, out=o, lse=lse, workspace=ws)
+
+            t_a, t_d = (timed(f, max(args.iters, 30), do_flush=False) for f in (app, dec))
+            emit({"kind": "paged", "shape": f"B{B} Hq{Hq} Hkv{Hkv} L{L} D{D} page{page}", "dtype": "bf16",
+                  "append_us": t_a * 1e3, "decode_us": t_d * 1e3, "gbs": 4 * B * Hkv * L * D / t_d / 1e6})
+            # the same batch behind one shared cache of this length, 64 rows each of their own
+            own = [torch.randn(B * n + B, Hkv, page, D, device=dev, generator=gen).to(torch.bfloat16) for _ in range(2)]
+            ids = torch.arange(B * n + B, device=dev, dtype=torch.int32)
+            both = torch.cat([ids[:n].expand(B, n), ids[B * n:, None]], 1).contiguous()
+            longer = lens + page
+            wp = torch.empty(fa.fa_decode_prefix_workspace_size(B, Hq, Hkv, L, D), device=dev, dtype=torch.uint8)
+            t_p = timed(lambda i: fa.decode_prefix(rq, *own, both, longer, L, out=o, lse=lse, workspace=wp),
+                        max(args.iters, 30), do_flush=False)
+            emit({"kind": "prefix", "shape": f"B{B} Hq{Hq} Hkv{Hkv} shared{L} own{page} D{D} page{page}",
+                  "dtype": "bf16", "us": t_p * 1e3, "tflops": 4 * B * Hq * (L + page) * D / t_p / 1e9})
+        for B, Hq, Hkv, S, D in ((1, 32, 32, 4096, 128), (4, 16, 16, 8192, 128)):
+            sets = [[torch.randn(B, S, h, D, device=dev).to(torch.bfloat16).transpose(1, 2) for h in (Hq, Hkv)]
+                    for _ in range(2)]
+            outs = [torch.empty(B, h, S, D, device=dev, dtype=torch.bfloat16) for h in (Hq, Hkv)]
+            freqs, amp = fa.rope_freqs(D, device=dev)
+            t_r = timed(lambda i: fa.rope(*sets[i % 2], freqs, amp=amp, out=tuple(outs)), max(args.iters, 30),
+                        do_flush=False)
+            emit({"kind": "rope", "shape": f"B{B} Hq{Hq} Hkv{Hkv} S{S} D{D} from [B, S, H, D]", "dtype": "bf16",
+                  "us": t_r * 1e3, "gbs": 4 * B * (Hq + Hkv) * S * D / t_r / 1e6})
 
 
 if __name__ == "__main__":
