@@ -20,12 +20,11 @@
 //
 // A CTA has one producer warp, which fills a ring of stages (a tile's K and V
 // rows) by TMA, a box per page, and runs ahead of the consumers over unit
-// boundaries; and four consumer warps, each with 16 rows of every tile.  Three
-// CTAs share an SM (two for groups above 8 with D = 128): what a unit costs
-// besides its rows (queries in, four warps' parts joined, a result out: about
-// 2.8 us) is latency, and the other CTAs' streams cover it.  One CTA of eight
-// consumer warps with the same 192 KB in flight took 28 us instead of 21 for 64
-// sequences of up to 512 rows.  The products are formed transposed,
+// boundaries; and four consumer warps, each with 16 rows of every tile.  Two CTAs
+// share an SM: what a unit costs besides its rows (queries in, four warps' parts
+// joined, a result out) is latency, and the other CTA's stream covers it.  One
+// CTA of eight consumer warps with the same 192 KB in flight took 28 us instead
+// of 23 for 64 sequences of up to 512 rows.  The products are formed transposed,
 // S^T = K Q^T and O^T = V^T P^T, with the cache rows (then the head's columns)
 // as the 16-row side of m16n8k16: a group of up to 8 query heads then pads to
 // 8 instead of 16, and one ldmatrix feeds a whole operand.
@@ -119,8 +118,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uin
 // that one copy brings whole rows and leaves them as [group][half][8][128
 // bytes]: 8-row groups D / 64 KB apart, whatever the page size, each half an
 // atom of the 128-byte swizzle.  (Boxes of 64 columns x rows need two copies
-// for D = 128; with 16-row pages the copies, at about 65 ns each an SM, then
-// bound decode at 4.1 to 4.6 TB/s.)
+// for D = 128; with 16-row pages the 2 KB copies bound
+// decode at 4.1 to 4.6 TB/s: 64 ragged sequences 233 us instead of 179.)
 __device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* m, uint64_t* bar, int group, int page) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"

@@ -6,8 +6,8 @@
 // over the cache.  Row (b, g) sees the first min(P, len_b) shared rows.  Each
 // CTA runs two tiles of up to 128 query rows over a contiguous range of
 // 128-row K/V tiles and writes normalised fp32 parts with the log2 of their
-// sums; paged_kernel and paged_merge_kernel join them with the rows that each
-// sequence has of its own.
+// sums; paged_kernel takes the rows that each sequence has of its own, and
+// paged_join_kernel joins both.
 //
 // Bound: with R = B * G rows a KV head, 4 R D flop against 4 D bytes a shared
 // row: HBM up to about 256 rows (the two tiles' products and exponentials of a

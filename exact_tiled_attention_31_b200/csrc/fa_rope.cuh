@@ -22,8 +22,8 @@
 // likewise of the copied part) for four heads, all of whose loads are in
 // flight before it forms the eight sines and cosines.  Four heads to a block,
 // and 128 threads, not more: the angles are cheap, and many short blocks leave
-// a short tail (q and k of 32 heads x 4096 rows: 24.0 us with 256 threads and
-// eight heads, 23.7 with four, 22.8 with 128 threads).  Where the heads of a
+// a short tail (q and k of 32 heads x 4096 rows, now 22.1 us; when tried:
+// 24.0 with 256 threads and eight heads, 23.7 with four, 22.8 with 128 threads).  Where the heads of a
 // token lie next to each other, neighbouring blocks take the heads of the same
 // tokens instead of the next tokens (22.4 us; with rows of a head next to each
 // other that costs 1 %: 81.0 against 80.2 us for 64 heads x 8192 twice).
