@@ -265,6 +265,8 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   if (Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;
   if (prefix_len % pages->page_size || prefix_len > max_len) return FA_ERR_INVALID_ARG;
   if ((long long)B * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  // paged_kernel counts what it has to do in 31 bits, whatever the lengths are
+  if ((long long)B * Hkv > 0x7fffffffLL / ((max_len + 63LL) / 64 + fa::kUnitCost)) return FA_ERR_UNSUPPORTED;
   if (!ptrs_ok({q, o, lse}) || !seq_lens || !ints_ok(seq_lens) || !ints_ok(prefix_table)) return FA_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_INVALID_ARG;
   const PagedWs w = paged_layout(B, Hq, Hkv, prefix_len, D);

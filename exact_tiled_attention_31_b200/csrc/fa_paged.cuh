@@ -102,8 +102,7 @@ struct PagedCfg {
   static_assert(CTAS * (SMEM + STATIC + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413,
-                PAGED_SITE_ROWS = 0x414 };
+enum : uint32_t { PAGED_SITE_FULL = 0x410, PAGED_SITE_EMPTY = 0x411, PAGED_SITE_DRAIN = 0x412, PAGED_SITE_PAGE = 0x413 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
@@ -393,7 +392,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
         const int b = EACH * lane + k, end = b < p.B ? length_of(b) : 0;
         n[k] = b < p.B ? tiles_of(end) + kUnitCost : 0;
         ends[b] = end;
-        mine += n[k];  // below 2^30 / 64 each
+        mine += n[k];
         most = max(most, n[k]);
       }
       int incl = mine;
@@ -446,11 +445,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- producer
-    total *= p.Hkv;
-    if (total >= 1LL << 31) {  // more rows than a call takes: hours of work, nothing is written
-      if (c == 0 && lane == 0) record_error(DEV_ERR_ARG, PAGED_SITE_ROWS);
-      total = 0;
-    }
+    total *= p.Hkv;  // below 2^31 with every length at its longest (paged_call)
     const long long units = (long long)p.B * p.Hkv;
     const PagedRuns runs((int)total, units, p.grid, p.next_run != nullptr);
     const bool whole = units <= p.grid && most <= kWholeTiles + kUnitCost;  // the same in every CTA: a unit each
@@ -913,8 +908,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p) {
 // each a share of the parts.  Bound: the n_pre + 1 fp32 parts of every row read
 // once, from L2 mostly; with few rows their latency, hence the split (2048 rows
 // of 17 parts took 8 us with a warp each, 14 warps to an SM).  (Joining inside
-// paged_kernel put this latency into every unit's chain: 5 us a unit with 9
-// parts.)
+// paged_kernel put this latency into every unit's chain.)
 template <int D, bool BF16, int SPLIT>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   constexpr int VEC = D / 32, ROWS = 8 / SPLIT;

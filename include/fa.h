@@ -448,9 +448,8 @@ fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, 
  * lengths on the device, so one recorded graph serves all lengths; which SM
  * takes what does not change the result, so equal calls on one GPU give equal
  * bits.  The workspace may be reused once the call's work on `stream` has
- * finished; calls that run at the same time need one each.  Heads * (rows / 64
- * + 3), summed over the sequences, may be at most 2^31 (checked on the device:
- * nothing is written and fa_check_device_error() returns FA_ERR_INVALID_ARG).
+ * finished; calls that run at the same time need one each.  B * Hkv *
+ * (max_pages * page_size / 64 + 2) must be below 2^31 (FA_ERR_UNSUPPORTED).
  * One to three kernel launches on `stream`.
  */
 /* The two-phase size query ("ops-transformer里的完整算子"); the size is for the

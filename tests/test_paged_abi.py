@@ -159,6 +159,21 @@ def test_decode_refusals_and_workspace():
         assert both("prefix", **bad) == {E}, bad
 
 
+def test_decode_refuses_tables_of_too_many_tiles():
+    """KV heads x sequences x (tiles of a full table + 2) is counted in 31 bits
+    by the kernels.  128 sequences of 2^30 rows sum to 2^31 + 256 for one head,
+    which is negative in 32 bits: refused before anything is launched."""
+    def status(B, Hkv, prefix):
+        pg = pages(stride=Hkv * 4096 * 128, row=1 << 18, page=4096, heads=Hkv, most=1 << 18)
+        q, end = (A, pg, A), (A, A, B, Hkv, 128, 0.1, 0, A, 0, None)  # no room: what is not refused ends there
+        return fa.fa_decode_paged(*q, *end) if prefix is None else fa.fa_decode_prefix(*q, prefix, None, *end)
+    for prefix in (None, 0, 4096):
+        for B, Hkv in ((128, 1), (64, 4), (300, 2)):
+            assert status(B, Hkv, prefix) == U, (B, Hkv, prefix)
+        for B in (127, 1):  # 127 * (2^24 + 2) < 2^31
+            assert status(B, 1, prefix) == E, (B, prefix)
+
+
 # ---------------------------------------------------------------- refusals of the tensor calls
 
 def test_tensor_calls_want_cuda_tensors():
