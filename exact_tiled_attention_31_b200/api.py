@@ -879,7 +879,8 @@ def decode_prefix(q, k_pages, v_pages, block_table, seq_lens, prefix_len: int, p
                   scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
     """``decode_paged`` for sequences whose first ``prefix_len`` rows (a
     multiple of the page size) are the same pages: those named by
-    ``prefix_table``, or by the first row of ``block_table``.  The shared rows
+    ``prefix_table``, or by ``block_table`` for the first sequence that has
+    them all (its other rows are not asked for them).  The shared rows
     are read once for the whole batch and must be finite, those that only
     longer sequences see too."""
     return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, int(prefix_len), prefix_table, scale, out, lse,

@@ -275,8 +275,7 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   fa::PagedParams p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.seq_lens = seq_lens;
-  const int* shared = prefix_table ? prefix_table : pages->block_table;  // the first sequence's row
-  p.map = {pages->block_table, pages->table_stride, pages->n_pages, log2_of(pages->page_size), max_len, shared,
+  p.map = {pages->block_table, pages->table_stride, pages->n_pages, log2_of(pages->page_size), max_len, prefix_table,
            prefix_len};
   p.o_part = reinterpret_cast<float*>(ws + w.o_part);
   p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
@@ -294,7 +293,6 @@ fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, 
   fa::PrefixParams pre = {};
   pre.seq_lens = seq_lens;
   pre.map = p.map;
-  pre.map.table = shared;
   pre.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
   pre.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
   pre.P = prefix_len, pre.n_pre = w.n_pre, pre.n_pairs = w.n_pairs, pre.per_tile = w.per_tile;

@@ -39,7 +39,7 @@ struct PagedMap {       // how rows of a sequence are found
   const int* table;     // [B, max_pages] by table_stride
   long long table_stride;
   int n_pages, page_shift, max_len;  // max_len: rows the table holds
-  const int* shared;    // the pages of the first n_shared rows of every sequence
+  const int* shared;    // the pages of the first n_shared rows of every sequence; null: those of shared_row's row of the table
   int n_shared;
 };
 
@@ -171,6 +171,25 @@ __device__ __forceinline__ int page_ok(const PagedMap& m, int id) {
   if (id >= 0 && id < m.n_pages) return id;
   record_error(DEV_ERR_ARG, PAGED_SITE_PAGE);
   return m.n_pages;
+}
+
+// Whose row of the table names the pages of the first n_shared rows: the first
+// sequence that has them all (so a padding row, or a row left over from a
+// sequence that has gone, is not asked), else the first of the longest, which
+// has every shared row that any sequence sees.  `rows` of them it has.  By all
+// lanes of a warp; len(b) is the length of sequence b.
+struct SharedRow {
+  int b, rows;
+};
+template <typename L>
+__device__ __forceinline__ SharedRow shared_row(int B, int n_shared, int lane, L&& len) {
+  SharedRow best{0, -1};
+  for (int b0 = 0; b0 < B && best.rows < n_shared; b0 += 32) {
+    const int b = b0 + lane, rows = b < B ? min(len(b), n_shared) : -1;
+    const int most = __reduce_max_sync(0xffffffffu, rows);
+    if (most > best.rows) best = SharedRow{b0 + __ffs(__ballot_sync(0xffffffffu, rows == most)) - 1, most};
+  }
+  return best;
 }
 
 // A row joined from parts: a lane holds VEC columns of it.
@@ -454,6 +473,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
       at.end = chunk == 1 ? ends[at.b] : length_of(at.b);
       at.tiles = tiles_of(at.end);
     };
+    const int* shared = p.map.shared;
+    if (p.map.n_shared && !p.n_pre && !shared)
+      shared = p.map.table + p.map.table_stride *
+               shared_row(p.B, p.map.n_shared, lane, [&](int b) { return chunk == 1 ? ends[b] : length_of(b); }).b;
     // The first tile of run c and the cost of what the run holds from it on.
     // Tile k of a unit sits kUnitCost + k behind the unit's start; there are at
     // most as many runs as there is cost, so no run inside a unit is without a
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
           const int i = k + lane / boxes;
           const int first = p.start + (at.tile + i) * C::KT + (lane % boxes) * box;
           return i < n && lane < batch * boxes && first < at.end
-                     ? (first < p.map.n_shared ? p.map.shared : row)[first >> p.map.page_shift]
+                     ? (first < p.map.n_shared ? shared : row)[first >> p.map.page_shift]
                      : -1;
         };
         int ids = find(0);

@@ -29,7 +29,7 @@ namespace fa {
 
 struct PrefixParams {
   const int* seq_lens;  // [B]
-  PagedMap map;         // table: the shared rows' pages; max_len clamps seq_lens
+  PagedMap map;         // n_shared: P; max_len clamps seq_lens
   float* pre_o;         // [n_pre, B * Hq, D]
   float* pre_lse;       // [n_pre, B * Hq]
   int P, n_pre, n_pairs;
@@ -143,10 +143,18 @@ __global__ void __launch_bounds__(768, 1)
       const int box = min(128, 1 << p.map.page_shift), boxes = 128 / box;  // rows per box, boxes per tile: <= 8
       const int my_box = (int)lane;
       const bool active = my_box < boxes;
-      // page of this lane's box of tile j; past the shared rows zeros are filled
+      // page of this lane's box of tile j; past the shared rows that there are zeros are filled
+      const int* shared = p.map.shared;
+      int rows = p.P;
+      if (!shared) {
+        const SharedRow from =
+            shared_row(p.B, p.P, (int)lane, [&](int b) { return min(max(p.seq_lens[b], 0), p.map.max_len); });
+        shared = p.map.table + from.b * p.map.table_stride;
+        rows = from.rows;
+      }
       auto find = [&](int j) {
         const int first = (j0 + j) * 128 + my_box * box;
-        return active && j < n_kv && first < p.P ? page_ok(p.map, p.map.table[first >> p.map.page_shift]) : p.map.n_pages;
+        return active && j < n_kv && first < rows ? page_ok(p.map, shared[first >> p.map.page_shift]) : p.map.n_pages;
       };
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);

@@ -464,7 +464,9 @@ fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_l
  *   prefix_len    a multiple of page_size, 0 <= prefix_len <= max_pages *
  *                 page_size (0: fa_decode_paged)
  *   prefix_table  DEVICE int32 [prefix_len / page_size], the shared rows'
- *                 pages; NULL: those of block_table's first row
+ *                 pages; NULL: those that block_table names for the first
+ *                 sequence of at least prefix_len rows (if there is none, for
+ *                 the first of the longest)
  * block_table and seq_lens are those of fa_decode_paged: rows from prefix_len
  * on are found in each sequence's own row of the table, and a sequence shorter
  * than prefix_len sees the first len_b shared rows.  Every shared row must

@@ -1,0 +1,89 @@
+"""Edges of the rotary and paged calls: whose row of the table names the shared
+pages, rows that nobody or only some may see, extreme scores, rows that a call
+skips, outputs that overlap."""
+import numpy as np
+import pytest
+import torch
+
+import exact_tiled_attention_31_b200 as fa
+from helpers import O_MAX
+from paged_helpers import U, check_decode, f64, freqs_of, make_cache, randn
+from oracle import paged as op
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x, dev):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+# Sequences that share 320 rows of 2 KV heads of 128: shorter than them, as long
+# and longer.  Once, the shared rows are read for each sequence; nine times over
+# they take a pass of their own; 16 times over there are more sequences than
+# threads that sum their lengths.
+P, PAGE, HQ, HKV, D = 320, 32, 8, 2, 128
+LENS = [0, 1, 31, 64, 129, 319, 320, 321, 400]
+
+
+def _batch(many, lens=LENS, seed=5):
+    gen = torch.Generator().manual_seed(seed)
+    lens = list(lens) * many
+    kp, vp, table = make_cache(gen, lens, HKV, D, PAGE, "bf16", shared=P // PAGE)
+    return lens, kp, vp, table, randn(gen, "bf16", len(lens), HQ, D)
+
+
+def _prefix(dev, lens, kp, vp, table, q, prefix_table=None):
+    o, lse = fa.decode_prefix(q.to(dev), kp.to(dev), vp.to(dev), table.to(dev), _i32(lens, dev), P,
+                              prefix_table=None if prefix_table is None else prefix_table.to(dev))
+    fa.check_device_error()
+    return o, lse
+
+
+# ---------------------------------------------------------------- whose pages are the shared ones
+
+@pytest.mark.parametrize("many", [1, 9, 16])
+@pytest.mark.parametrize("first", ["none", "other pages", "its own rows alone"])
+def test_shared_pages_without_the_first_sequence(cuda_device, many, first):
+    """No prefix_table, and the first sequence is a padding row (its table row
+    -1, or left over from other sequences) or shorter than the shared rows (-1
+    behind its length): the pages are those of a sequence that has them all."""
+    lens, kp, vp, table, q = _batch(many, LENS if first != "its own rows alone" else LENS[3:] + LENS[:3])
+    given = table.clone()
+    if first == "none":
+        given[0] = -1
+    elif first == "other pages":
+        given[0] = given[8].flip(0)
+    for b, n in enumerate(lens):  # entries past a length are never read, the shared ones neither
+        if n < P and not (b == 0 and first == "other pages"):
+            given[b, -(-n // PAGE):] = -1
+    o, lse = _prefix(cuda_device, lens, kp, vp, given, q)
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, D ** -0.5), first)
+
+
+@pytest.mark.parametrize("many", [1, 30])
+def test_shared_pages_that_no_sequence_has_all_of(cuda_device, many):
+    """Every sequence ends inside the shared rows: the longest one's pages are theirs, its entries behind -1."""
+    lens, kp, vp, table, q = _batch(many, [0, 17, 300, 288, 40])
+    given = table.clone()
+    for b, n in enumerate(lens):
+        given[b, -(-n // PAGE):] = -1
+    o, lse = _prefix(cuda_device, lens, kp, vp, given, q)
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, D ** -0.5), "all of them shorter")
+    o, lse = _prefix(cuda_device, [0] * len(lens), kp, vp, torch.full_like(table, -1), q)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_row_of_the_table_among_many_sequences(cuda_device):
+    """600 sequences read their shared rows one by one; the only one that has them all comes late."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(2)
+    shared, page = 64, 16
+    lens = [i % 60 for i in range(600)]
+    lens[417] = 90
+    kp, vp, table = make_cache(gen, lens, 1, 64, page, "fp16", shared=shared // page)
+    q = randn(gen, "fp16", len(lens), 3, 64)
+    given = table.clone()
+    given[:417, :4] = -1
+    given[418:, :4] = -1
+    o, lse = fa.decode_prefix(q.to(dev), kp.to(dev), vp.to(dev), given.to(dev), _i32(lens, dev), shared)
+    fa.check_device_error()
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, 0.125), "one full sequence")
