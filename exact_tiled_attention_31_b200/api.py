@@ -881,8 +881,8 @@ def decode_prefix(q, k_pages, v_pages, block_table, seq_lens, prefix_len: int, p
     multiple of the page size) are the same pages: those named by
     ``prefix_table``, or by ``block_table`` for the first sequence that has
     them all (its other rows are not asked for them).  The shared rows
-    are read once for the whole batch and must be finite, those that only
-    longer sequences see too."""
+    are read once for the whole batch; a sequence shorter than ``prefix_len``
+    sees those up to its length, whatever the others hold."""
     return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, int(prefix_len), prefix_table, scale, out, lse,
                          workspace, stream)
 

@@ -105,7 +105,7 @@ int prefix_splits(long long units, int P) {
   const long long tiles = ((long long)P + 127) / 128, sms = sm_count();
   if (tiles <= 0) return 0;
   long long best = 1, cost = -1;
-  for (long long n = 1; n <= std::min(64LL, tiles); ++n) {
+  for (long long n = 1; n <= std::min((long long)fa::kMaxRanges, tiles); ++n) {
     const long long c = ((units * n + sms - 1) / sms) * ((tiles + n - 1) / n + 4);
     if (cost < 0 || c < cost) best = n, cost = c;
   }
@@ -176,20 +176,22 @@ bool map_queries(CUtensorMap* m, const void* q, int B, int Hkv, int G, int D, bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tiles of the longest sequence that the table can hold, and whether a call may
-// hand out runs (which takes one more small launch, about 1 us).
+// Tiles behind the shared rows of the longest sequence that the table can hold
+// (one that ends inside them has at most a range of them to read, which is no
+// reason for more CTAs), and whether a call may hand out runs (which takes one
+// more small launch, about 1 us).
 long long paged_tiles(const fa::PagedParams& p) { return std::max(1, (p.map.max_len - p.start + 63) / 64); }
 bool hands_out(const fa::PagedParams& p, long long tiles) {
   return (long long)p.B * p.Hkv * tiles >= fa::kClaimTiles * kPagedCtas * sm_count();
 }
 
-template <int D, bool BF16, int NB>
+template <int D, bool BF16, int NB, bool PRE>
 fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_t st) {
   using C = fa::PagedCfg<D, NB>;
   CUtensorMap mk, mv;
   const int box = std::min(C::KT, pg.page_size);
   if (!map_pages(&mk, pg.k, pg, D, BF16, box) || !map_pages(&mv, pg.v, pg, D, BF16, box)) return FA_ERR_CUDA;
-  if (set_smem<fa::paged_kernel<D, BF16, NB>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  if (set_smem<fa::paged_kernel<D, BF16, NB, PRE>>(C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
   fa::PagedParams a = p;
   const long long tiles = paged_tiles(p);
   static_assert(C::CTAS == kPagedCtas && C::KT == 64, "workspace for every run");
@@ -197,16 +199,16 @@ fa_status launch_paged(const fa::PagedParams& p, const fa_pages& pg, cudaStream_
   a.grid = (int)std::min(ctas, units * tiles);
   const bool claim = hands_out(p, tiles);
   a.max_runs = claim ? a.grid * fa::PagedRuns::kMaxWaves : a.grid;
-  a.by_unit = p.n_pre || units <= a.max_runs;
+  a.by_unit = PRE || units <= a.max_runs;
   if (!claim) a.next_run = nullptr;
   // (behind shared rows the count was zeroed before them)
-  if (claim && !p.n_pre) {
+  if (claim && !PRE) {
     const fa_status s = launch_after(fa::paged_zero_kernel, dim3(1), 32, 0, st, a.next_run);
     if (s != FA_OK) return s;
   }
-  const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
+  const fa_status s = launch_after(fa::paged_kernel<D, BF16, NB, PRE>, dim3(a.grid), C::THREADS, C::SMEM, st, mk, mv, a);
   if (s != FA_OK) return s;
-  if (p.n_pre) {
+  if constexpr (PRE) {
     // four warps a row while all of them run at once (eight blocks to an SM)
     const long long rows = (long long)p.B * p.Hq;
     if (rows <= 16LL * sm_count() && p.n_pre >= 4)
@@ -246,8 +248,9 @@ fa_status run_paged(const fa::PagedParams& p, const fa::PrefixParams& pre, const
     }
     const fa_status s = launch_prefix<D, BF16>(pre, q, pg, st);
     if (s != FA_OK) return s;
+    return p.G <= 8 ? launch_paged<D, BF16, 1, true>(p, pg, st) : launch_paged<D, BF16, 2, true>(p, pg, st);
   }
-  return p.G <= 8 ? launch_paged<D, BF16, 1>(p, pg, st) : launch_paged<D, BF16, 2>(p, pg, st);
+  return p.G <= 8 ? launch_paged<D, BF16, 1, false>(p, pg, st) : launch_paged<D, BF16, 2, false>(p, pg, st);
 }
 
 fa_status paged_call(const void* q, const fa_pages* pages, const int* seq_lens, int prefix_len, const int* prefix_table,

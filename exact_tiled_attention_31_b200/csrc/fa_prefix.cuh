@@ -3,7 +3,8 @@
 // The first P rows of every sequence are the same pages.  For one KV head the
 // B sequences' G query heads each are then B * G query rows against one and
 // the same K and V: a matrix product, as in the forward, instead of B passes
-// over the cache.  Row (b, g) sees the first min(P, len_b) shared rows.  Each
+// over the cache.  Row (b, g) takes the ranges that lie whole in [0, len_b);
+// paged_kernel reads the rows of the one that the sequence ends in.  Each
 // CTA runs two tiles of up to 128 query rows over a contiguous range of
 // 128-row K/V tiles and writes normalised fp32 parts with the log2 of their
 // sums; paged_kernel takes the rows that each sequence has of its own, and
@@ -70,8 +71,9 @@ __global__ void __launch_bounds__(768, 1)
   const int rest = blockIdx.x / p.n_pairs;
   const int kvh = rest % p.Hkv, split = rest / p.Hkv;
   const int all_tiles = (p.P + 127) / 128;
-  const int j0 = (int)((long long)split * all_tiles / p.n_pre);
-  const int n_kv = (int)((long long)(split + 1) * all_tiles / p.n_pre) - j0;  // >= 1: n_pre <= all_tiles
+  const int j0 = range_begin(split, all_tiles, p.n_pre);
+  const int n_kv = range_begin(split + 1, all_tiles, p.n_pre) - j0;  // >= 1: n_pre <= all_tiles
+  const int range_end = min(p.P, 128 * (j0 + n_kv));
   const int b0 = 2 * pair * p.per_tile;  // first sequence of query tile 0; tile 1 follows
   const bool has_t1 = b0 + p.per_tile < p.B;
   const int n0 = n_kv, n1 = has_t1 ? n_kv : 0;
@@ -143,18 +145,31 @@ __global__ void __launch_bounds__(768, 1)
       const int box = min(128, 1 << p.map.page_shift), boxes = 128 / box;  // rows per box, boxes per tile: <= 8
       const int my_box = (int)lane;
       const bool active = my_box < boxes;
-      // page of this lane's box of tile j; past the shared rows that there are zeros are filled
-      const int* shared = p.map.shared;
-      int rows = p.P;
-      if (!shared) {
-        const SharedRow from =
-            shared_row(p.B, p.P, (int)lane, [&](int b) { return min(max(p.seq_lens[b], 0), p.map.max_len); });
-        shared = p.map.table + from.b * p.map.table_stride;
-        rows = from.rows;
-      }
+      // table entry of this lane's box of tile j; past the shared rows zeros are filled
+      const int* shared = p.map.shared ? p.map.shared : p.map.table;
       auto find = [&](int j) {
         const int first = (j0 + j) * 128 + my_box * box;
-        return active && j < n_kv && first < rows ? page_ok(p.map, shared[first >> p.map.page_shift]) : p.map.n_pages;
+        return active && j < n_kv && first < p.P ? shared[first >> p.map.page_shift] : p.map.n_pages;
+      };
+      auto length_of = [&](int b) { return min(p.seq_lens[b], p.map.max_len); };
+      // The first sequence's entries are on their way while its length shows
+      // whether they are the ones.
+      int id0 = find(0), id1 = find(1);
+      if (!p.map.shared && length_of(0) < p.P) {
+        shared += shared_row(p.seq_lens, p.B, p.map.max_len, p.P) * p.map.table_stride;
+        id0 = find(0);
+        id1 = find(1);
+      }
+      // The page of an entry, or zeros where it names none: an error where a
+      // sequence of this CTA takes the range (entries that none has may be anything).
+      auto page_of = [&](int j, int id) {
+        const bool none = (id < 0 || id >= p.map.n_pages) && active && (j0 + j) * 128 + my_box * box < p.P;
+        if (__any_sync(0xffffffffu, none)) {
+          bool taken = false;
+          for (int b = b0 + (int)lane; b < min(b0 + 2 * p.per_tile, p.B); b += 32) taken |= length_of(b) >= range_end;
+          if (__any_sync(0xffffffffu, taken) && none) record_error(DEV_ERR_ARG, PAGED_SITE_PAGE);
+        }
+        return id >= 0 && id < p.map.n_pages ? id : p.map.n_pages;
       };
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -184,12 +199,11 @@ __global__ void __launch_bounds__(768, 1)
         }
         ++fill;
       };
-      int id0 = find(0), id1 = find(1);
-      load(false, 0, id0);
+      load(false, 0, page_of(0, id0));
       for (int jj = 0; jj < n_kv && ok; ++jj) {
         const int id2 = find(jj + 2);
-        load(true, jj, id0);
-        if (ok && jj + 1 < n_kv) load(false, jj + 1, id1);
+        load(true, jj, page_of(jj, id0));
+        if (ok && jj + 1 < n_kv) load(false, jj + 1, page_of(jj + 1, id1));
         id0 = id1;
         id1 = id2;
       }
@@ -285,9 +299,9 @@ __global__ void __launch_bounds__(768, 1)
     const float sl2 = p.scale_log2;
     float* my_max = pmax_buf + (2 * t + h) * 128 + r;
     const float* other_max = pmax_buf + (2 * t + (h ^ 1)) * 128 + r;
-    // shared rows that this query row sees
+    // the range's end, if this query row takes it
     const int b = seq_of_row(t, r);
-    const int sees = b >= 0 ? min(p.P, min(max(p.seq_lens[b], 0), p.map.max_len)) : 0;
+    const int sees = b >= 0 && min(p.seq_lens[b], p.map.max_len) >= range_end ? range_end : 0;
     float m = -INFINITY, l = 0.f, lr = 0.f;
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {

@@ -358,7 +358,7 @@ typedef struct {
  *   block_table DEVICE int32 [B, max_pages], rows table_stride elements apart:
  *               row i of sequence b is row i % page_size of page
  *               block_table[b][i / page_size].  Entries past a sequence's
- *               length are never read.
+ *               length may hold anything.
  *   page_size   a power of two, 16 to 4096 (FA_ERR_UNSUPPORTED otherwise)
  * max_pages * page_size may be at most 2^30. */
 typedef struct {
@@ -468,11 +468,11 @@ fa_status fa_decode_paged(const void* q, const fa_pages* pages, const int* seq_l
  *                 sequence of at least prefix_len rows (if there is none, for
  *                 the first of the longest)
  * block_table and seq_lens are those of fa_decode_paged: rows from prefix_len
- * on are found in each sequence's own row of the table, and a sequence shorter
- * than prefix_len sees the first len_b shared rows.  Every shared row must
- * hold finite values.  Where reading the shared rows for each sequence is
- * sooner done (up to three sequences, or 24 MB more to read), that is what the
- * call does.  One to four kernel launches on `stream`.
+ * on are found in each sequence's own row of the table.  A sequence shorter
+ * than prefix_len sees the first len_b shared rows.  With up to three
+ * sequences, or up to 24 MB more to read, the shared rows are read for each
+ * sequence instead; the result is that of fa_decode_paged either way, rounded
+ * in another order.  One to four kernel launches on `stream`.
  */
 /* The two-phase size query ("ops-transformer里的完整算子"), for the current device. */
 size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int D);

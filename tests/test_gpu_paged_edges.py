@@ -87,3 +87,63 @@ def test_row_of_the_table_among_many_sequences(cuda_device):
     o, lse = fa.decode_prefix(q.to(dev), kp.to(dev), vp.to(dev), given.to(dev), _i32(lens, dev), shared)
     fa.check_device_error()
     check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, 0.125), "one full sequence")
+
+
+# ---------------------------------------------------------------- what is in rows that a sequence does not see
+
+@pytest.mark.parametrize("many", [1, 9])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_values_in_shared_rows_that_some_do_not_see(cuda_device, many, bad):
+    """A value that is not finite reaches the sequences that see its row and no
+    others, whether or not the shared rows take a pass of their own."""
+    lens, kp, vp, table, q = _batch(many)
+    ref = op.decode_paged(q, kp, vp, table.numpy(), lens, D ** -0.5)
+    at, col = 200, 77
+    vp[table[8, at // PAGE], 1, at % PAGE, col] = bad
+    o, lse = _prefix(cuda_device, lens, kp, vp, table, q)
+    hit = torch.zeros(o.shape, dtype=torch.bool, device=o.device)
+    for b, n in enumerate(lens):
+        hit[b, HQ // HKV:, col] = n > at
+    assert hit.any() and not torch.isfinite(o[hit]).any()
+    want = torch.from_numpy(ref[0]).to(o.device)
+    check_decode(torch.where(hit, want.to(o.dtype), o), lse, q, ref, f"{bad} in one row")
+
+
+@pytest.mark.parametrize("many", [1, 30])
+def test_shared_rows_behind_every_length(cuda_device, many):
+    """Shared rows at and past the longest length hold NaN."""
+    lens, kp, vp, table, q = _batch(many, [0, 17, 300, 288, 40])
+    for x in (kp, vp):
+        x[table[0, 9], :, 300 % PAGE:] = float("nan")  # rows 300 to 319
+    o, lse = _prefix(cuda_device, lens, kp, vp, table, q, prefix_table=table[0, :P // PAGE].clone())
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, D ** -0.5), "NaN behind every length")
+
+
+@pytest.mark.parametrize("many", [1, 9])
+def test_shared_pages_named_by_one_row_alone(cuda_device, many):
+    """The first sequence that has all shared rows names them; every other row of the table holds -1 there."""
+    lens, kp, vp, table, q = _batch(many)
+    given = table.clone()
+    given[[b for b in range(len(lens)) if b != 6], :P // PAGE] = -1
+    o, lse = _prefix(cuda_device, lens, kp, vp, given, q)
+    check_decode(o, lse, q, op.decode_paged(q, kp, vp, table.numpy(), lens, D ** -0.5), "one row of the table")
+
+
+@pytest.mark.parametrize("many", [4, 81])
+def test_bad_shared_page_is_reported_where_it_is_seen(cuda_device, many):
+    """A shared page outside the pool: an error if a sequence sees its rows, none if all end in front of it."""
+    dev = cuda_device
+    for n, seen in ((128, False), (P, True)):
+        lens, kp, vp, table, q = _batch(1, [n, 128] * (many // 2) + [n] * (many % 2))
+        prefix = table[0, :P // PAGE].clone()
+        prefix[7] = kp.shape[0]  # rows 224 to 255
+        o, lse = fa.decode_prefix(q.to(dev), kp.to(dev), vp.to(dev), table.to(dev), _i32(lens, dev), P,
+                                  prefix_table=prefix.to(dev))
+        if seen:
+            with pytest.raises(fa.FAError) as e:
+                fa.check_device_error()
+            assert e.value.status == fa.api.FA_ERR_INVALID_ARG
+        fa.check_device_error()
+        short = [b for b in range(len(lens)) if lens[b] == 128]
+        ref = op.decode_paged(q[short], kp, vp, table[short].numpy(), [128] * len(short), D ** -0.5)
+        check_decode(o[short], lse[short], q[short], ref, "the sequences in front of it")
