@@ -147,3 +147,51 @@ def test_bad_shared_page_is_reported_where_it_is_seen(cuda_device, many):
         short = [b for b in range(len(lens)) if lens[b] == 128]
         ref = op.decode_paged(q[short], kp, vp, table[short].numpy(), [128] * len(short), D ** -0.5)
         check_decode(o[short], lse[short], q[short], ref, "the sequences in front of it")
+
+
+# ---------------------------------------------------------------- extreme scores
+
+def _score_rows(scores):
+    """Keys whose product with a query of ones in its first three columns is the score, to 2^-24 of it."""
+    k = torch.zeros(len(scores), 64)
+    rest = torch.tensor(scores, dtype=torch.float64)
+    for i in range(3):
+        k[:, i] = rest.to(torch.bfloat16).float()
+        rest = rest - k[:, i].double()
+    return k.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("up", [7.0, 0.0])
+def test_two_keys_of_nearly_one_weight(cuda_device, up):
+    """Two keys share the weight; in log2 units one is 2^-8 + 2^-14, the other
+    2^-8 - 2^-14 above 2^`up` times the largest weight in front of them, which
+    is just above and just below a midpoint of bf16.  Relative to the exact
+    maximum the larger weight is exactly 1 and the other within 2^-8, so O is
+    off by at most w1 w2 2^-8 |v1 - v2| (w1 + w2 <= 1, w1 w2 <= 1 / 4) beside
+    its own half step: 2^-7 for values of +-4, within the 1e-2 that forward and
+    decode are held to.  Relative to an older maximum both would round, apart:
+    2^-6."""
+    dev = cuda_device
+    B, Hkv, page, rows = 130, 8, 64, 8192
+    scores = np.full(rows, -60.0)
+    ln2 = np.log(2.0)
+    scores[np.arange(40, 63) * 128] = 0.0
+    one, two = 63 * 128 + 5, 63 * 128 + 70
+    for at, d in ((one, -1), (two, 1)):
+        scores[at] = (up + np.log2(1 + 2.0 ** -8 + d * 2.0 ** -14)) * ln2
+    k, v = _score_rows(scores), torch.zeros(rows, 64)
+    v[one], v[two] = 4.0, -4.0
+    kp, vp = (x.to(torch.bfloat16).view(rows // page, 1, page, 64).expand(-1, Hkv, -1, -1).contiguous().to(dev)
+              for x in (k, v))
+    q = torch.zeros(B, Hkv, 64, dtype=torch.bfloat16)
+    q[..., :3] = 1.0
+    table = torch.arange(rows // page, dtype=torch.int32, device=dev).expand(B, -1).contiguous()
+    args = (q.to(dev), kp, vp, table, _i32([rows] * B, dev))
+    w = np.exp(k[:, :3].double().sum(-1).numpy())
+    ref = 4.0 * (w[one] - w[two]) / w.sum()
+    tol = 0.25 * 2.0 ** -8 * 8.0 + 2.0 ** -8 * abs(ref) + 2.0 ** -18
+    assert tol < O_MAX
+    for o, lse in (fa.decode_prefix(*args, rows, scale=1.0), fa.decode_paged(*args, scale=1.0)):
+        fa.check_device_error()
+        assert np.abs(f64(o) - ref).max() <= tol, (f64(o).flat[0], ref, tol)
+        assert np.abs(f64(lse) - np.log(w.sum())).max() <= 1e-5
