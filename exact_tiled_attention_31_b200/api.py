@@ -35,7 +35,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_varlen", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd
            "fa_bwd_finish", "fa_bwd_noalloc", "fa_bwd_varlen_workspace_size", "fa_bwd_varlen", "fa_status_string",
            "fa_check_device_error", "fa_launch_count", "fa_selftest_timeout", "fa_decode_num_splits",
            "fa_decode_workspace_size", "fa_decode", "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_varlen_dropout",
-           "fa_bwd_varlen_dropout", "fa_rope_freqs", "fa_rope", "fa_append_paged", "fa_decode_paged_workspace_size",
+           "fa_bwd_varlen_dropout", "fa_rope_freqs", "fa_rope", "fa_rope_fill", "fa_append_paged", "fa_append_paged_fill",
+           "fa_decode_paged_workspace_size",
            "fa_decode_paged", "fa_decode_prefix_workspace_size", "fa_decode_prefix")
 
 # fa_rope_scaling, and the layouts of the structs fa_rows and fa_pages of include/fa.h
@@ -113,8 +114,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_rope_freqs.restype = i
     lib.fa_rope.argtypes = [vp, vp, i, vp, i, i, f, i, vp, i64, vp, i, i, i, i, i, vp]
     lib.fa_rope.restype = i
+    lib.fa_rope_fill.argtypes, lib.fa_rope_fill.restype = lib.fa_rope.argtypes, i
     lib.fa_append_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, vp, i, i, f, vp, i, i, vp]
     lib.fa_append_paged.restype = i
+    lib.fa_append_paged_fill.argtypes, lib.fa_append_paged_fill.restype = lib.fa_append_paged.argtypes, i
     lib.fa_decode_paged_workspace_size.argtypes = [i, i, i, i]
     lib.fa_decode_paged_workspace_size.restype = sz
     lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, i, i, i, f, i, vp, sz, vp]
@@ -232,11 +235,23 @@ def fa_rope(x, y, n, freqs, rot_dim, interleaved, amp, backward, positions, posi
                                   positions_stride, cu_seqlens, nseq, B, S, D, dt, stream)
 
 
+def fa_rope_fill(x, y, n, freqs, rot_dim, interleaved, amp, backward, positions, positions_stride, cu_seqlens, nseq, B,
+                 S, D, dt, stream) -> int:
+    return load_library().fa_rope_fill(x, y, n, freqs, rot_dim, int(interleaved), amp, int(backward), positions,
+                                       positions_stride, cu_seqlens, nseq, B, S, D, dt, stream)
+
+
 def fa_append_paged(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim, interleaved, amp,
                     positions, D, dt, stream) -> int:
     """``k``, ``v``, ``q``, ``q_out``: the bytes of one ``fa_rows`` each, ``pages``: of an ``fa_pages``."""
     return load_library().fa_append_paged(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim,
                                           int(interleaved), amp, positions, D, dt, stream)
+
+
+def fa_append_paged_fill(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim, interleaved, amp,
+                         positions, D, dt, stream) -> int:
+    return load_library().fa_append_paged_fill(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim,
+                                               int(interleaved), amp, positions, D, dt, stream)
 
 
 def fa_decode_paged_workspace_size(B, Hq, Hkv, D) -> int:
@@ -681,8 +696,9 @@ def _rope_call(raw, known, q, k, freqs, positions, cu_seqlens, interleaved, amp,
             if ykp == yp and ykp:
                 raise ValueError("the two outputs are the same memory")
     if not empty:
-        st = _lib.fa_rope(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions),
-                          pos_stride, _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
+        call = _lib.fa_rope if given else _lib.fa_rope_fill
+        st = call(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions), pos_stride,
+                  _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
         if st != FA_OK:
             raise FAError(st, "fa_rope")
     return yq, yk
@@ -694,7 +710,8 @@ def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved: bool = False
     tensors, or packed [H, T, D] ones with ``cu_seqlens``.  Inputs may be any
     views whose rows are contiguous (a transposed projection, say); the
     outputs are contiguous, or ``out`` = (q_out, k_out), which may be the
-    inputs themselves.  ``freqs`` and ``amp`` come from ``rope_freqs``;
+    inputs themselves.  Rows behind the last sequence are zero in new outputs
+    and left as they were in ``out``.  ``freqs`` and ``amp`` come from ``rope_freqs``;
     ``positions`` (int32 [S] or [B, S]; packed [T]) defaults to the index in
     the sequence.  The columns past the rotated ones are copied."""
     return _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, False)
@@ -775,7 +792,8 @@ def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
     (CUDA int32 [B]) are the lengths with the new tokens, as ``decode_paged``
     takes them next.  Without ``freqs`` nothing is rotated.  Returns the
     rotated q (``q_out``, which may be q) or None.  Tokens of a sequence of
-    length 0 and tokens behind the last sequence write nothing; a row past
+    length 0 and tokens behind the last sequence write nothing (their rows of
+    a new q are zero); a row past
     the table or a page outside the pool is reported by
     ``check_device_error``."""
     known = _known(
@@ -797,11 +815,11 @@ def _append_call(raw, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_s
         if q_out is not None:
             _apart(xp, yp, q_rows)
         qx, qy = _ROWS.pack(xp, *q_rows[0]), _ROWS.pack(yp, *q_rows[1])
-    if T and B:
-        st = _lib.fa_append_paged(_ROWS.pack(k.data_ptr(), *k_rows), _ROWS.pack(v.data_ptr(), *v_rows), qx, qy,
-                                  _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(),
-                                  _ptr(cu_seqlens), B, T, _ptr(freqs), rot, interleaved, amp, _ptr(positions), D, dt,
-                                  raw)
+    if T:
+        call = _lib.fa_append_paged_fill if q_out is None else _lib.fa_append_paged
+        st = call(_ROWS.pack(k.data_ptr(), *k_rows), _ROWS.pack(v.data_ptr(), *v_rows), qx, qy,
+                  _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(), _ptr(cu_seqlens), B, T,
+                  _ptr(freqs), rot, interleaved, amp, _ptr(positions), D, dt, raw)
         if st != FA_OK:
             raise FAError(st, "fa_append_paged")
     return to

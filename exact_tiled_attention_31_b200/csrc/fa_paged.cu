@@ -76,21 +76,88 @@ dim3 rope_grid(long long rows, int groups, long long head_stride, long long row_
 }
 
 template <int D, bool BF16>
-fa_status launch_rope(fa::RopeParams& p, bool inter, cudaStream_t st) {
+fa_status launch_rope(fa::RopeParams& p, bool inter, bool fill, cudaStream_t st) {
   if ((long long)p.B * p.S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const dim3 grid = rope_grid<D>((long long)p.B * p.S, fa::rope_groups(p.heads[0]) + fa::rope_groups(p.heads[1]), p.x[0].head, p.x[0].row, p.heads_near);
-  return launch_after(inter ? fa::rope_kernel<D, BF16, true> : fa::rope_kernel<D, BF16, false>, grid, fa::kRopeThreads,
-                      0, st, p);
+  const auto kern = fill ? (inter ? fa::rope_kernel<D, BF16, true, true> : fa::rope_kernel<D, BF16, false, true>)
+                         : (inter ? fa::rope_kernel<D, BF16, true, false> : fa::rope_kernel<D, BF16, false, false>);
+  return launch_after(kern, grid, fa::kRopeThreads, 0, st, p);
 }
 
 template <int D, bool BF16>
-fa_status launch_append(fa::AppendParams& p, bool inter, cudaStream_t st) {
+fa_status launch_append(fa::AppendParams& p, bool inter, bool fill, cudaStream_t st) {
   const dim3 grid = rope_grid<D>(p.T, fa::rope_groups(p.Hq) + 2 * fa::rope_groups(p.Hkv), p.k.head, p.k.row, p.heads_near);
-  return launch_after(inter ? fa::append_kernel<D, BF16, true> : fa::append_kernel<D, BF16, false>, grid,
-                      fa::kRopeThreads, 0, st, p);
+  const auto kern = fill ? (inter ? fa::append_kernel<D, BF16, true, true> : fa::append_kernel<D, BF16, false, true>)
+                         : (inter ? fa::append_kernel<D, BF16, true, false> : fa::append_kernel<D, BF16, false, false>);
+  return launch_after(kern, grid, fa::kRopeThreads, 0, st, p);
 }
 
 bool rot_ok(int rot_dim, int D) { return rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0; }
+
+// fill: rows of no sequence become zero
+fa_status rope_call(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
+                    float amp, int backward, const int* positions, long long positions_stride, const int* cu_seqlens,
+                    int nseq, int B, int S, int D, fa_dtype dt, void* stream, bool fill) {
+  if (B < 0 || S < 0 || nseq < 0 || positions_stride < 0 || n < 1 || n > 2 || !x || !y) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
+  if (cu_seqlens && B > 1) return FA_ERR_INVALID_ARG;
+  if (B == 0 || S == 0 || (cu_seqlens && nseq == 0 && !fill)) return FA_OK;
+  if (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 7u) || !ints_ok(positions) || !ints_ok(cu_seqlens))
+    return FA_ERR_INVALID_ARG;
+  fa::RopeParams p = {};
+  for (int i = 0; i < n; ++i) {
+    if (!rows_ok(&x[i]) || !rows_ok(&y[i]) || x[i].heads != y[i].heads) return FA_ERR_INVALID_ARG;
+    p.x[i] = rows_in(x[i]);
+    p.y[i] = rows_out(y[i]);
+    p.heads[i] = x[i].heads;
+  }
+  if ((long long)p.heads[0] + p.heads[1] > 65535) return FA_ERR_UNSUPPORTED;
+  p.freqs = freqs, p.positions = positions, p.pos_batch = positions_stride;
+  p.cu = cu_seqlens, p.nseq = nseq, p.B = B, p.S = S, p.R = rot_dim;
+  p.amp = amp, p.sign = backward ? -1.f : 1.f;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool in = interleaved != 0, zero = fill && cu_seqlens;
+  if (D == 128) return dt == FA_BF16 ? launch_rope<128, true>(p, in, zero, st) : launch_rope<128, false>(p, in, zero, st);
+  return dt == FA_BF16 ? launch_rope<64, true>(p, in, zero, st) : launch_rope<64, false>(p, in, zero, st);
+}
+
+fa_status append_call(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out, const fa_pages* pages,
+                      const int* seq_lens, const int* cu_seqlens, int nseq, int total, const double* freqs, int rot_dim,
+                      int interleaved, float amp, const int* positions, int D, fa_dtype dt, void* stream, bool fill) {
+  if (nseq < 0 || total < 0) return FA_ERR_INVALID_ARG;
+  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (freqs && !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && nseq != total) return FA_ERR_INVALID_ARG;
+  if (fill && q && nseq == 0)  // every row is one of no sequence
+    return rope_call(q, q_out, 1, freqs, rot_dim, interleaved, amp, 0, nullptr, 0, cu_seqlens, 0, 1, total, D, dt, stream,
+                     true);
+  if (nseq == 0 || total == 0) return FA_OK;
+  const fa_status s = pages_check(pages, D);
+  if (s != FA_OK) return s;
+  if (!rows_ok(k) || !rows_ok(v) || k->heads != pages->heads || v->heads != pages->heads) return FA_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q) || !rows_ok(q_out) || q->heads != q_out->heads || !freqs)) return FA_ERR_INVALID_ARG;
+  if (!seq_lens || !ints_ok(seq_lens) || !ints_ok(cu_seqlens) || !ints_ok(positions) ||
+      (reinterpret_cast<uintptr_t>(freqs) & 7u))
+    return FA_ERR_INVALID_ARG;
+  fa::AppendParams p = {};
+  p.k = rows_in(*k), p.v = rows_in(*v);
+  if (q) p.q = rows_in(*q), p.q_out = rows_out(*q_out), p.Hq = q->heads;
+  if ((long long)p.Hq + 2LL * pages->heads > 65535) return FA_ERR_UNSUPPORTED;
+  p.k_pages = static_cast<uint16_t*>(pages->k);
+  p.v_pages = static_cast<uint16_t*>(pages->v);
+  p.page_stride = pages->page_stride, p.table = pages->block_table, p.table_stride = pages->table_stride;
+  p.n_pages = pages->n_pages, p.page_shift = log2_of(pages->page_size), p.max_pages = pages->max_pages;
+  p.seq_lens = seq_lens, p.cu = cu_seqlens, p.freqs = freqs, p.positions = positions;
+  p.nseq = nseq, p.T = total, p.Hkv = pages->heads, p.R = freqs ? rot_dim : 0, p.amp = amp;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool in = interleaved != 0, zero = fill && q;
+  if (D == 128) return dt == FA_BF16 ? launch_append<128, true>(p, in, zero, st) : launch_append<128, false>(p, in, zero, st);
+  return dt == FA_BF16 ? launch_append<64, true>(p, in, zero, st) : launch_append<64, false>(p, in, zero, st);
+}
 
 // ---------------------------------------------------------------- paged decode
 constexpr int kPagedCtas = 2;  // of paged_kernel on an SM
@@ -354,65 +421,33 @@ fa_status fa_rope_freqs(int rot_dim, double base, fa_rope_scaling scaling, doubl
 }
 
 fa_status fa_rope(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
-                  float amp, int backward, const int* positions, long long positions_stride, const int* cu_seqlens,
-                  int nseq, int B, int S, int D, fa_dtype dt, void* stream) {
-  if (B < 0 || S < 0 || nseq < 0 || positions_stride < 0 || n < 1 || n > 2 || !x || !y) return FA_ERR_INVALID_ARG;
-  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
-  if (cu_seqlens && B > 1) return FA_ERR_INVALID_ARG;
-  if (B == 0 || S == 0 || (cu_seqlens && nseq == 0)) return FA_OK;
-  if (!freqs || (reinterpret_cast<uintptr_t>(freqs) & 7u) || !ints_ok(positions) || !ints_ok(cu_seqlens))
-    return FA_ERR_INVALID_ARG;
-  fa::RopeParams p = {};
-  for (int i = 0; i < n; ++i) {
-    if (!rows_ok(&x[i]) || !rows_ok(&y[i]) || x[i].heads != y[i].heads) return FA_ERR_INVALID_ARG;
-    p.x[i] = rows_in(x[i]);
-    p.y[i] = rows_out(y[i]);
-    p.heads[i] = x[i].heads;
-  }
-  if ((long long)p.heads[0] + p.heads[1] > 65535) return FA_ERR_UNSUPPORTED;
-  p.freqs = freqs, p.positions = positions, p.pos_batch = positions_stride;
-  p.cu = cu_seqlens, p.nseq = nseq, p.B = B, p.S = S, p.R = rot_dim;
-  p.amp = amp, p.sign = backward ? -1.f : 1.f;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool in = interleaved != 0;
-  if (D == 128) return dt == FA_BF16 ? launch_rope<128, true>(p, in, st) : launch_rope<128, false>(p, in, st);
-  return dt == FA_BF16 ? launch_rope<64, true>(p, in, st) : launch_rope<64, false>(p, in, st);
+                  float amp, int backward, const int* positions, long long positions_stride,
+                  const int* cu_seqlens, int nseq, int B, int S, int D, fa_dtype dt, void* stream) {
+  return rope_call(x, y, n, freqs, rot_dim, interleaved, amp, backward, positions, positions_stride, cu_seqlens, nseq, B,
+                   S, D, dt, stream, false);
+}
+
+fa_status fa_rope_fill(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
+                       float amp, int backward, const int* positions, long long positions_stride,
+                       const int* cu_seqlens, int nseq, int B, int S, int D, fa_dtype dt, void* stream) {
+  return rope_call(x, y, n, freqs, rot_dim, interleaved, amp, backward, positions, positions_stride, cu_seqlens, nseq, B,
+                   S, D, dt, stream, true);
 }
 
 fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
-                          const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
-                          const double* freqs, int rot_dim, int interleaved, float amp, const int* positions, int D,
-                          fa_dtype dt, void* stream) {
-  if (nseq < 0 || total < 0) return FA_ERR_INVALID_ARG;
-  if (dt != FA_BF16 && dt != FA_FP16) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(amp)) return FA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  if (freqs && !rot_ok(rot_dim, D)) return FA_ERR_UNSUPPORTED;
-  if (!cu_seqlens && nseq != total) return FA_ERR_INVALID_ARG;
-  if (nseq == 0 || total == 0) return FA_OK;
-  const fa_status s = pages_check(pages, D);
-  if (s != FA_OK) return s;
-  if (!rows_ok(k) || !rows_ok(v) || k->heads != pages->heads || v->heads != pages->heads) return FA_ERR_INVALID_ARG;
-  if (q && (!rows_ok(q) || !rows_ok(q_out) || q->heads != q_out->heads || !freqs)) return FA_ERR_INVALID_ARG;
-  if (!seq_lens || !ints_ok(seq_lens) || !ints_ok(cu_seqlens) || !ints_ok(positions) ||
-      (reinterpret_cast<uintptr_t>(freqs) & 7u))
-    return FA_ERR_INVALID_ARG;
-  fa::AppendParams p = {};
-  p.k = rows_in(*k), p.v = rows_in(*v);
-  if (q) p.q = rows_in(*q), p.q_out = rows_out(*q_out), p.Hq = q->heads;
-  if ((long long)p.Hq + 2LL * pages->heads > 65535) return FA_ERR_UNSUPPORTED;
-  p.k_pages = static_cast<uint16_t*>(pages->k);
-  p.v_pages = static_cast<uint16_t*>(pages->v);
-  p.page_stride = pages->page_stride, p.table = pages->block_table, p.table_stride = pages->table_stride;
-  p.n_pages = pages->n_pages, p.page_shift = log2_of(pages->page_size), p.max_pages = pages->max_pages;
-  p.seq_lens = seq_lens, p.cu = cu_seqlens, p.freqs = freqs, p.positions = positions;
-  p.nseq = nseq, p.T = total, p.Hkv = pages->heads, p.R = freqs ? rot_dim : 0, p.amp = amp;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool in = interleaved != 0;
-  if (D == 128) return dt == FA_BF16 ? launch_append<128, true>(p, in, st) : launch_append<128, false>(p, in, st);
-  return dt == FA_BF16 ? launch_append<64, true>(p, in, st) : launch_append<64, false>(p, in, st);
+                          const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq,
+                          int total, const double* freqs, int rot_dim, int interleaved, float amp,
+                          const int* positions, int D, fa_dtype dt, void* stream) {
+  return append_call(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim, interleaved, amp,
+                     positions, D, dt, stream, false);
+}
+
+fa_status fa_append_paged_fill(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
+                               const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq,
+                               int total, const double* freqs, int rot_dim, int interleaved, float amp,
+                               const int* positions, int D, fa_dtype dt, void* stream) {
+  return append_call(k, v, q, q_out, pages, seq_lens, cu_seqlens, nseq, total, freqs, rot_dim, interleaved, amp,
+                     positions, D, dt, stream, true);
 }
 
 size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int D) {

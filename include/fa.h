@@ -411,6 +411,12 @@ fa_status fa_rope(const fa_rows* x, const fa_rows* y, int n, const double* freqs
                   float amp, int backward, const int* positions, long long positions_stride, const int* cu_seqlens,
                   int nseq, int B, int S, int D, fa_dtype dt, void* stream);
 
+/* fa_rope for outputs that hold nothing yet: rows of no sequence (with nseq = 0
+ * all of them) become zero instead of being left as they were. */
+fa_status fa_rope_fill(const fa_rows* x, const fa_rows* y, int n, const double* freqs, int rot_dim, int interleaved,
+                       float amp, int backward, const int* positions, long long positions_stride,
+                       const int* cu_seqlens, int nseq, int B, int S, int D, fa_dtype dt, void* stream);
+
 /*
  * New keys and values into the pages of their sequences, keys rotated on the
  * way, and the queries of the same tokens rotated by the same launch.
@@ -432,6 +438,13 @@ fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, 
                           const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
                           const double* freqs, int rot_dim, int interleaved, float amp, const int* positions, int D,
                           fa_dtype dt, void* stream);
+
+/* fa_append_paged for a q_out that holds nothing yet: the rows of tokens that
+ * write nothing become zero in it. */
+fa_status fa_append_paged_fill(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
+                               const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
+                               const double* freqs, int rot_dim, int interleaved, float amp, const int* positions,
+                               int D, fa_dtype dt, void* stream);
 
 /*
  * fa_decode over a paged cache: for b < B, h < Hq, G = Hq / pages->heads,

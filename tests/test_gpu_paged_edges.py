@@ -195,3 +195,72 @@ def test_two_keys_of_nearly_one_weight(cuda_device, up):
         fa.check_device_error()
         assert np.abs(f64(o) - ref).max() <= tol, (f64(o).flat[0], ref, tol)
         assert np.abs(f64(lse) - np.log(w.sum())).max() <= 1e-5
+
+
+# ---------------------------------------------------------------- rows that a call skips
+
+def _leave_nan(shape, dev):
+    """What the next allocation of this size finds in its memory."""
+    torch.cuda.synchronize()
+    x = [torch.full(shape, float("nan"), dtype=torch.bfloat16, device=dev) for _ in range(4)]
+    torch.cuda.synchronize()
+    del x
+
+
+@pytest.mark.parametrize("call", ["rope", "rope_backward"])
+@pytest.mark.parametrize("lens,tail", [([5, 0, 40], 19), ([0], 7), ([], 5), ([64], 0)])
+def test_rows_of_no_sequence_in_new_outputs_are_zero(cuda_device, call, lens, tail):
+    """Rows behind the last sequence of outputs that the call allocates hold
+    zeros, so that a product over all rows (a weight's gradient) stays finite."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(1)
+    n, T = sum(lens), sum(lens) + tail
+    q, k = randn(gen, "bf16", 6, T, 128).to(dev), randn(gen, "bf16", 2, T, 128).to(dev)
+    freqs = torch.from_numpy(freqs_of(64)).to(dev)
+    cu = _i32(np.concatenate([[0], np.cumsum(lens)]), dev)
+    for x in (q, k):
+        _leave_nan(x.shape, dev)
+    got = getattr(fa, call)(q, k, freqs, cu_seqlens=cu)
+    given = tuple(torch.full_like(x, 3.0) for x in (q, k))
+    getattr(fa, call)(q, k, freqs, cu_seqlens=cu, out=given)
+    fa.check_device_error()
+    for x, y in zip(got, given):
+        assert (x[:, n:] == 0).all() and torch.equal(x[:, :n], y[:, :n]) and (y[:, n:] == 3.0).all()
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_queries_of_padding_tokens_in_new_outputs_are_zero(cuda_device, one):
+    """append_paged without q_out: the queries of tokens that are not written are zero, and with q_out left as they were."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(4)
+    lens = [3, 0, 17, 0] if one else [3, 0, 17]
+    new = [1] * 4 if one else [5, 2, 4]  # two tokens in front of the first sequence's rows, two of an empty one
+    cu = np.concatenate([[0], np.cumsum(new)])
+    T = int(cu[-1]) + (0 if one else 3)  # three behind the last sequence
+    skipped = [1, 3] if one else [0, 1, 5, 6, 11, 12, 13]
+    kp, vp, table = (x.to(dev) for x in make_cache(gen, [max(n, 1) for n in lens], 2, 64, 16, "bf16", poison=False))
+    shape = (lambda h: (T, h, 64)) if one else (lambda h: (h, T, 64))
+    q, k, v = (randn(gen, "bf16", *shape(h)).to(dev) for h in (5, 2, 2))
+    kw = dict(q=q, freqs=torch.from_numpy(freqs_of(32)).to(dev), cu_seqlens=None if one else _i32(cu, dev))
+    _leave_nan(q.shape, dev)
+    got = fa.append_paged(k, v, kp, vp, table, _i32(lens, dev), **kw)
+    given = torch.full_like(q, 3.0)
+    fa.append_paged(k, v, kp, vp, table, _i32(lens, dev), q_out=given, **kw)
+    fa.check_device_error()
+    got, given = (x if one else x.transpose(0, 1) for x in (got, given))
+    rest = [t for t in range(T) if t not in skipped]
+    assert (got[skipped] == 0).all() and (given[skipped] == 3.0).all() and torch.equal(got[rest], given[rest])
+    assert torch.isfinite(given).all() and not (given[rest] == 3.0).all()
+
+
+def test_queries_of_no_sequences_are_zero(cuda_device):
+    """Tokens without any sequence: append_paged writes nothing, and zeros to a new q."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(4)
+    q, k = randn(gen, "bf16", 4, 9, 64).to(dev), randn(gen, "bf16", 2, 9, 64).to(dev)
+    kp, vp = (torch.full((3, 2, 16, 64), 2.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    args = (k, k, kp, vp, torch.zeros(0, 3, dtype=torch.int32, device=dev), torch.zeros(0, dtype=torch.int32, device=dev))
+    kw = dict(cu_seqlens=_i32([0], dev), freqs=torch.from_numpy(freqs_of(32)).to(dev))
+    _leave_nan(q.shape, dev)
+    assert (fa.append_paged(*args, q=q, **kw) == 0).all() and fa.append_paged(*args, **kw) is None
+    given = torch.full_like(q, 3.0)
+    fa.append_paged(*args, q=q, q_out=given, **kw)
+    fa.check_device_error()
+    assert (given == 3.0).all() and (kp == 2.0).all() and (vp == 2.0).all()
