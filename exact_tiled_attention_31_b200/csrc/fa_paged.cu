@@ -3,6 +3,7 @@
 // launch configuration.  The kernels are in fa_rope.cuh, fa_paged.cuh and
 // fa_prefix.cuh.
 #include <algorithm>
+#include <utility>
 
 #include "fa_host.cuh"
 #include "fa_prefix.cuh"
@@ -22,6 +23,102 @@ fa::RowsIn rows_in(const fa_rows& r) {
 }
 fa::RowsOut rows_out(const fa_rows& r) {
   return {static_cast<uint16_t*>(r.data), r.batch_stride, r.head_stride, r.row_stride};
+}
+
+// ---------------------------------------------------------------- overlaps
+// What a call reads or writes of a strided stack: `run` contiguous 16-bit
+// values at `at` plus every sum of index * stride, strides falling.
+struct Stack {
+  uintptr_t at;
+  long long run;
+  int dims;
+  bool repeats;  // an index that moves nothing (a broadcast)
+  struct {
+    long long n, stride, inner;  // inner: from the first to behind the last value of one index
+  } dim[3];
+  long long extent() const { return dims ? dim[0].inner + (dim[0].n - 1) * dim[0].stride : run; }
+};
+
+Stack stack_of(const void* data, long long run, std::initializer_list<std::pair<long long, long long>> dims) {
+  Stack s = {reinterpret_cast<uintptr_t>(data), run, 0, false, {}};
+  for (const auto& [n, stride] : dims) {
+    if (n > 1 && stride == 0) s.repeats = true;
+    if (n <= 1 || stride == 0) continue;
+    int i = s.dims++;
+    for (; i > 0 && s.dim[i - 1].stride < stride; --i) s.dim[i] = s.dim[i - 1];
+    s.dim[i] = {n, stride, 0};
+  }
+  long long inner = run;
+  for (int i = s.dims - 1; i >= 0; --i) {
+    s.dim[i].inner = inner;
+    inner += (s.dim[i].n - 1) * s.dim[i].stride;
+  }
+  return s;
+}
+
+long long floor_div(long long a, long long b) { return a / b - (a % b != 0 && a < 0); }
+
+// Whether some run of a (from dimension i on, delta values behind b's start)
+// meets one of b (from dimension j on); of one stack with itself (self) only
+// where the indices differ.  Where the outer strides are equal only the
+// difference of the two indices counts, and of nested strides (views of one
+// buffer) only a few can bring the inner parts together; else the indices of
+// one of them are tried.  `tries` bounds that: what has used it up counts as
+// overlapping.
+bool meet(const Stack& a, int i, const Stack& b, int j, long long delta, bool self, int& tries) {
+  const long long ea = i < a.dims ? a.dim[i].inner + (a.dim[i].n - 1) * a.dim[i].stride : a.run;
+  const long long eb = j < b.dims ? b.dim[j].inner + (b.dim[j].n - 1) * b.dim[j].stride : b.run;
+  if (delta >= eb || -delta >= ea) return false;
+  if (--tries < 0) return true;
+  if (i == a.dims && j == b.dims) return !self;
+  if (i < a.dims && j < b.dims && a.dim[i].stride == b.dim[j].stride) {
+    const auto &da = a.dim[i], &db = b.dim[j];
+    // -inner of a < delta + d * stride < inner of b
+    const long long lo = std::max(-(db.n - 1), floor_div(-da.inner - delta, da.stride) + 1);
+    const long long hi = std::min(da.n - 1, floor_div(db.inner - delta - 1, da.stride));
+    for (long long d = lo; d <= hi; ++d)
+      if (meet(a, i + 1, b, j + 1, delta + d * da.stride, self && d == 0, tries)) return true;
+    return false;
+  }
+  if (j == b.dims || (i < a.dims && a.dim[i].stride > b.dim[j].stride)) {
+    const auto& da = a.dim[i];
+    const long long lo = std::max(0LL, floor_div(-da.inner - delta, da.stride) + 1);
+    const long long hi = std::min(da.n - 1, floor_div(eb - delta - 1, da.stride));
+    for (long long d = lo; d <= hi; ++d)
+      if (meet(a, i + 1, b, j, delta + d * da.stride, self, tries)) return true;
+    return false;
+  }
+  const auto& db = b.dim[j];
+  const long long lo = std::max(0LL, floor_div(delta - db.inner, db.stride) + 1);
+  const long long hi = std::min(db.n - 1, floor_div(delta + ea - 1, db.stride));
+  for (long long d = lo; d <= hi; ++d)
+    if (meet(a, i, b, j + 1, delta - d * db.stride, self, tries)) return true;
+  return false;
+}
+
+bool overlap(const Stack& a, const Stack& b) {
+  const long long ea = a.extent(), eb = b.extent();
+  if (a.at >= b.at + 2 * (unsigned long long)eb || b.at >= a.at + 2 * (unsigned long long)ea) return false;
+  int tries = 1 << 16;
+  return meet(a, 0, b, 0, ((long long)a.at - (long long)b.at) / 2, false, tries);
+}
+// whether two indices of an output lead to one place
+bool overlaps_itself(const Stack& a) {
+  if (a.repeats) return true;
+  bool nested = true;
+  for (int i = 0; i < a.dims; ++i) nested &= a.dim[i].stride >= a.dim[i].inner;
+  if (nested) return false;
+  int tries = 1 << 16;
+  return meet(a, 0, a, 0, 0, true, tries);
+}
+// the same rows, index by index: an output that is its input, in place
+bool in_place(const fa_rows& y, const fa_rows& x, int B, int S) {
+  return y.data == x.data && (B == 1 || y.batch_stride == x.batch_stride) &&
+         (y.heads == 1 || y.head_stride == x.head_stride) && (S == 1 || y.row_stride == x.row_stride);
+}
+// [batch, heads, rows] of D values
+Stack stack_of(const fa_rows& r, int B, int S, int D) {
+  return stack_of(r.data, D, {{B, r.batch_stride}, {r.heads, r.head_stride}, {S, r.row_stride}});
 }
 
 // Pages: a pool of n_pages x heads x page_size x D, 16-byte aligned; a table.
@@ -77,7 +174,6 @@ dim3 rope_grid(long long rows, int groups, long long head_stride, long long row_
 
 template <int D, bool BF16>
 fa_status launch_rope(fa::RopeParams& p, bool inter, bool fill, cudaStream_t st) {
-  if ((long long)p.B * p.S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const dim3 grid = rope_grid<D>((long long)p.B * p.S, fa::rope_groups(p.heads[0]) + fa::rope_groups(p.heads[1]), p.x[0].head, p.x[0].row, p.heads_near);
   const auto kern = fill ? (inter ? fa::rope_kernel<D, BF16, true, true> : fa::rope_kernel<D, BF16, false, true>)
                          : (inter ? fa::rope_kernel<D, BF16, true, false> : fa::rope_kernel<D, BF16, false, false>);
@@ -113,14 +209,23 @@ fa_status rope_call(const fa_rows* x, const fa_rows* y, int n, const double* fre
     p.y[i] = rows_out(y[i]);
     p.heads[i] = x[i].heads;
   }
-  if ((long long)p.heads[0] + p.heads[1] > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)p.heads[0] + p.heads[1] > 65535 || (long long)B * S > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  // an output is its own input, in place, or apart from everything else
+  Stack in[2], out[2];
+  for (int i = 0; i < n; ++i) in[i] = stack_of(x[i], B, S, D), out[i] = stack_of(y[i], B, S, D);
+  for (int i = 0; i < n; ++i) {
+    if (overlaps_itself(out[i])) return FA_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j)
+      if (!(i == j && in_place(y[i], x[i], B, S)) && overlap(out[i], in[j])) return FA_ERR_INVALID_ARG;
+  }
+  if (n == 2 && overlap(out[0], out[1])) return FA_ERR_INVALID_ARG;
   p.freqs = freqs, p.positions = positions, p.pos_batch = positions_stride;
   p.cu = cu_seqlens, p.nseq = nseq, p.B = B, p.S = S, p.R = rot_dim;
   p.amp = amp, p.sign = backward ? -1.f : 1.f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool in = interleaved != 0, zero = fill && cu_seqlens;
-  if (D == 128) return dt == FA_BF16 ? launch_rope<128, true>(p, in, zero, st) : launch_rope<128, false>(p, in, zero, st);
-  return dt == FA_BF16 ? launch_rope<64, true>(p, in, zero, st) : launch_rope<64, false>(p, in, zero, st);
+  const bool il = interleaved != 0, zero = fill && cu_seqlens;
+  if (D == 128) return dt == FA_BF16 ? launch_rope<128, true>(p, il, zero, st) : launch_rope<128, false>(p, il, zero, st);
+  return dt == FA_BF16 ? launch_rope<64, true>(p, il, zero, st) : launch_rope<64, false>(p, il, zero, st);
 }
 
 fa_status append_call(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out, const fa_pages* pages,
@@ -147,6 +252,19 @@ fa_status append_call(const fa_rows* k, const fa_rows* v, const fa_rows* q, cons
   p.k = rows_in(*k), p.v = rows_in(*v);
   if (q) p.q = rows_in(*q), p.q_out = rows_out(*q_out), p.Hq = q->heads;
   if ((long long)p.Hq + 2LL * pages->heads > 65535) return FA_ERR_UNSUPPORTED;
+  // the pools apart from each other (one pool for both only where it takes the
+  // same rows unrotated); q_out is q, in place, or apart from everything else
+  const long long page = (long long)pages->heads * pages->page_size * D;
+  const Stack pool_k = stack_of(pages->k, page, {{pages->n_pages, pages->page_stride}});
+  const Stack pool_v = stack_of(pages->v, page, {{pages->n_pages, pages->page_stride}});
+  const Stack ks = stack_of(*k, 1, total, D), vs = stack_of(*v, 1, total, D);
+  if (overlap(pool_k, pool_v) && (freqs || pages->k != pages->v || !in_place(*k, *v, 1, total))) return FA_ERR_INVALID_ARG;
+  if (q) {
+    const Stack qs = stack_of(*q, 1, total, D), to = stack_of(*q_out, 1, total, D);
+    if (overlaps_itself(to) || (!in_place(*q_out, *q, 1, total) && overlap(to, qs)) || overlap(to, ks) || overlap(to, vs) ||
+        overlap(to, pool_k) || overlap(to, pool_v))
+      return FA_ERR_INVALID_ARG;
+  }
   p.k_pages = static_cast<uint16_t*>(pages->k);
   p.v_pages = static_cast<uint16_t*>(pages->v);
   p.page_stride = pages->page_stride, p.table = pages->block_table, p.table_stride = pages->table_stride;

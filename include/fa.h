@@ -396,7 +396,8 @@ fa_status fa_rope_freqs(int rot_dim, double base, fa_rope_scaling scaling, doubl
  * (the angle negated): the gradient of x from that of y.
  *   x, y    n inputs and outputs with equal `heads`; y[i] may be x[i] itself
  *           (same data and strides), any other overlap of an output with an
- *           input or output is not allowed
+ *           input, an output or itself is refused (FA_ERR_INVALID_ARG); rows of
+ *           one buffer between one another (a fused projection) do not overlap
  *   freqs   DEVICE double [rot_dim / 2]; angles are reduced in fp64, so
  *           positions may be any int32
  *   dense   (cu_seqlens = NULL): [B, heads, S] rows; the position of row t is
@@ -421,7 +422,8 @@ fa_status fa_rope_fill(const fa_rows* x, const fa_rows* y, int n, const double* 
  * New keys and values into the pages of their sequences, keys rotated on the
  * way, and the queries of the same tokens rotated by the same launch.
  *   k, v      [heads, total] rows (batch_stride unused), heads = pages->heads
- *   q, q_out  [Hq, total] rows, or both NULL; q_out may be q itself
+ *   q, q_out  [Hq, total] rows, or both NULL; q_out may be q itself, and is
+ *             otherwise apart from q, k, v and the pools (FA_ERR_INVALID_ARG)
  *   seq_lens  DEVICE int32 [nseq]: each sequence's length with its new tokens
  *   cu_seqlens DEVICE int32 [nseq + 1]: token t is a new one of the sequence s
  *             with cu_seqlens[s] <= t < cu_seqlens[s + 1]; NULL: total = nseq
@@ -432,7 +434,10 @@ fa_status fa_rope_fill(const fa_rows* x, const fa_rows* y, int n, const double* 
  * must be NULL).  Tokens with i < 0 (padding: length 0) and tokens behind
  * cu_seqlens[nseq] write nothing.  A row past the table, or a page outside
  * [0, n_pages), is not written, and fa_check_device_error() then returns
- * FA_ERR_INVALID_ARG.  Two tokens of one call must not fall on one row.
+ * FA_ERR_INVALID_ARG.  Two tokens of one call must not fall on one row, and k,
+ * v and q must not be rows that the call writes.  The two pools may not overlap
+ * (FA_ERR_INVALID_ARG), but may be one where k and v are the same rows and
+ * nothing is rotated.
  */
 fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
                           const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,

@@ -264,3 +264,45 @@ def test_queries_of_no_sequences_are_zero(cuda_device):
     fa.append_paged(*args, q=q, q_out=given, **kw)
     fa.check_device_error()
     assert (given == 3.0).all() and (kp == 2.0).all() and (vp == 2.0).all()
+
+
+# ---------------------------------------------------------------- outputs that overlap
+
+def test_overlapping_outputs_are_refused(cuda_device):
+    """Each output is its own input, in place, or apart from everything else of the call."""
+    bf = dict(dtype=torch.bfloat16, device=cuda_device)
+    f = torch.ones(32, dtype=torch.float64, device=cuda_device)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=cuda_device)
+    q, k = (torch.randn(2, 4, 6, 64, **bf) for _ in range(2))
+    buf = torch.zeros(2, 8, 6, 64, **bf)
+    kp, vp = (torch.zeros(4, 2, 16, 64, **bf) for _ in range(2))
+    t, n = i32(2, 2), i32(2) + 1
+    t[1] = 1
+    k1, q1 = torch.zeros(2, 2, 64, **bf), torch.zeros(2, 4, 64, **bf)
+    one = torch.zeros(2, 8, 64, **bf)
+    wrong = [
+        lambda: fa.rope(q, k, f, out=(k, q)),                                  # exchanged
+        lambda: fa.rope(q, k, f, out=(torch.empty_like(q), q)),                # k_out on q
+        lambda: fa.rope(q, k, f, out=(buf[:, :4], buf[:, 2:6])),               # two outputs in part
+        lambda: fa.rope(q, None, f, out=buf.view(-1).as_strided((2, 4, 6, 64), (1536, 384, 32, 1))),  # of itself
+        lambda: fa.append_paged(k1, k1, kp, vp, t, n, q=one[:, :4], freqs=f, q_out=one[:, 2:6]),
+        lambda: fa.append_paged(one[:, 4:6], k1, kp, vp, t, n, q=q1, freqs=f, q_out=one[:, 4:]),      # on k
+        lambda: fa.append_paged(k1, one[:, 4:6], kp, vp, t, n, q=q1, freqs=f, q_out=one[:, 2:6]),     # on v
+        lambda: fa.append_paged(k1, k1, kp, kp, t, n, freqs=f),                # keys and values into one pool
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises((ValueError, fa.FAError)):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+    fa.check_device_error()
+    # one buffer of a fused projection, q and k in place or into another such buffer's places
+    fused, other = (torch.randn(2, 6, 12, 64, **bf) for _ in range(2))
+    parts = lambda x: (x[:, :, :8].transpose(1, 2), x[:, :, 8:10].transpose(1, 2))
+    want = fa.rope(*parts(fused), f)
+    rest = other[:, :, 10:].clone()
+    fa.rope(*parts(fused), f, out=parts(other))
+    fa.rope(*parts(fused), f, out=parts(fused))
+    fa.check_device_error()
+    for x in (fused, other):
+        assert all(torch.equal(a, b) for a, b in zip(parts(x), want))
+    assert torch.equal(other[:, :, 10:], rest)

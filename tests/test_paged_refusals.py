@@ -45,3 +45,105 @@ def test_fill_entries_refuse_what_the_plain_ones_refuse():
                positions=None, D=128, dt=0, stream=None)
     assert fa.fa_append_paged(rows(), rows(), rows(), None, **bad) == OK
     assert fa.fa_append_paged_fill(rows(), rows(), rows(), None, **bad) == E
+
+
+# ---------------------------------------------------------------- overlaps
+
+def _hit(call):
+    """Whether the call is refused.  What is not refused goes on to its launch, which fails here without a device."""
+    st = call()
+    assert st in (E, api.FA_ERR_CUDA), st
+    return st == E
+
+
+def _rope(x, y, B, S, D=64):
+    return lambda: fa.fa_rope(b"".join(x), b"".join(y), len(x), A, 64, 0, 1.0, 0, None, 0, None, 0, B, S, D, 0, None)
+
+
+def _places(r, B, S, D):
+    import numpy as np
+    data, batch, head, row, heads = api._ROWS.unpack(r)
+    at = data // 2 + np.add.outer(np.add.outer(np.add.outer(np.arange(B) * batch, np.arange(heads) * head),
+                                               np.arange(S) * row), np.arange(D))
+    return at.ravel()
+
+
+def _expected(x, y, B, S, D=64):
+    """By listing the elements: an output over itself, another output, or an input that it is not in place of."""
+    outs, ins = [_places(r, B, S, D) for r in y], [_places(r, B, S, D) for r in x]
+    if any(len(set(o)) < len(o) for o in outs):
+        return True
+    sets = [set(o) for o in outs]
+    for i, o in enumerate(sets):
+        for j in range(len(x)):
+            if not (i == j and (outs[i] == ins[j]).all()) and o & set(ins[j]):
+                return True
+    return len(y) == 2 and bool(sets[0] & sets[1])
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="addresses that no launch may see")
+def test_rope_overlaps_against_a_list_of_elements():
+    import random
+    rng = random.Random(11)
+    D, seen = 64, {True: 0, False: 0}
+    for _ in range(1500):
+        B, S, hq, hk = rng.choice([1, 2, 3]), rng.choice([1, 2, 5]), rng.choice([1, 2, 4]), rng.choice([1, 2])
+        x, y = [], []
+        n = rng.choice([1, 2])
+        kind = rng.choice(["fused", "fused", "arena", "any"])
+        for i, h in enumerate((hq, hk)[:n]):
+            both = []
+            for _ in range(2):
+                if kind == "fused":    # [B, S, 8 heads, D], some heads of it
+                    at, st = 64 * rng.randrange(0, 9 - h), (S * 8 * 64, 64, 8 * 64)
+                elif kind == "arena":  # a region of heads by rows or of rows by heads in each batch's 2048
+                    at, st = 64 * rng.choice([0, 2, 5, 10, 16, 20]), (2048, *rng.choice([(S * 64, 64), (64, h * 64)]))
+                else:
+                    at, st = 8 * rng.randrange(0, 60), tuple(8 * rng.choice([0, 1, 4, 8, 9, 16, 24, 40, 72]) for _ in range(3))
+                both.append(rows(A + 2 * at + (0 if rng.random() < 0.6 else 1 << 16), *st, h))
+            x.append(both[0])
+            y.append(both[0] if rng.random() < 0.4 else both[1])
+        want = _expected(x, y, B, S)
+        assert _hit(_rope(x, y, B, S)) == want, (kind, B, S, [api._ROWS.unpack(r) for r in x + y])
+        seen[want] += 1
+    assert min(seen.values()) > 300, seen
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="addresses that no launch may see")
+def test_rope_overlaps_of_large_buffers():
+    """A fused projection of 4 x 8192 tokens, in place: no overlap, found without a walk over its rows."""
+    import time
+    B, S, H = 4, 8192, 48
+    part = lambda first, heads, base=A: rows(base + 128 * first, S * H * 64, 64, H * 64, heads)
+    q, k, v = part(0, 32), part(32, 8), part(40, 8)
+    other = (part(0, 32, 1 << 40), part(32, 8, 1 << 40))
+    t = time.perf_counter()
+    for _ in range(100):
+        assert not _hit(_rope((q, k), (q, k), B, S)) and not _hit(_rope((q, k), other, B, S))
+    assert not _hit(_rope((q, k), (q, v), B, S))
+    assert time.perf_counter() - t < 5
+    for y in ((k, part(40, 8)), (q, part(31, 8)), (part(1, 32), k), (q, part(0, 8)), (part(8, 32), part(0, 8))):
+        assert _hit(_rope((q, k), y, B, S)), y
+    assert _hit(_rope((k, v), (v, k), B, S))                               # exchanged
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="addresses that no launch may see")
+def test_append_overlaps():
+    def call(k=rows(A, 0, 640, 64), v=rows(A + (1 << 20), 0, 640, 64), q=None, qo=None, pg=pages(k=1 << 40, v=1 << 41), f=A):
+        return lambda: fa.fa_append_paged(k, v, q, qo, pg, A, None, 10, 10, f, 64, 0, 1.0, None, 64, 0, None)
+    at = lambda first: rows(A + 2 * first, 0, 64, 1024, 4)                  # [10 tokens, 16 heads, 64], heads from first / 64 on
+    two = lambda first: rows(A + 2 * first, 0, 64, 1024, 2)
+    assert not _hit(call()) and not _hit(call(q=at(0), qo=at(0), k=two(256), v=two(384)))
+    assert not _hit(call(q=at(0), qo=at(512), k=two(256), v=two(384)))
+    for first in (64, 192, 256, 320, 384, 448):                            # on q in part, k, v
+        assert _hit(call(q=at(0), qo=at(first), k=two(256), v=two(384))), first
+    assert _hit(call(q=at(0), qo=rows(A + (1 << 30), 0, 32, 1024, 4)))      # on itself
+    assert _hit(call(q=at(0), qo=rows((1 << 40) + 4096, 0, 64, 1024, 4)))   # on the pools
+    assert _hit(call(q=at(0), qo=rows((1 << 41) + 4096, 0, 64, 1024, 4)))
+    page = 2 * 64 * 64
+    inter = pages(k=1 << 40, v=(1 << 40) + 2 * page, stride=2 * page)       # one allocation, page by page
+    assert not _hit(call(pg=inter))
+    assert _hit(call(pg=pages(k=1 << 40, v=(1 << 40) + page, stride=2 * page)))
+    one = pages(k=1 << 40, v=1 << 40)
+    same = dict(k=rows(A, 0, 640, 64), v=rows(A, 0, 640, 64), pg=one)
+    assert _hit(call(pg=one)) and _hit(call(**same)) and not _hit(call(**same, f=None))
