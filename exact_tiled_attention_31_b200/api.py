@@ -502,6 +502,14 @@ def _known(key, make, *args):
     return got
 
 
+def _c_int(x, what):
+    """``x`` as the C entries take it: ctypes would cut it to 32 bits without a word."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what} does not fit 32 bits: {x}")
+    return x
+
+
 def _sig(t):
     return None if t is None else (t.dtype, t.get_device(), t.shape, t.stride())
 
@@ -622,10 +630,11 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
     import torch
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
-    out = (ctypes.c_double * max(int(rot_dim) // 2, 1))()
+    rot_dim, original_len = _c_int(rot_dim, "rot_dim"), _c_int(original_len, "original_len")
+    out = (ctypes.c_double * max(rot_dim // 2, 1))()
     amp = ctypes.c_float()
-    st = fa_rope_freqs(int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor), int(original_len),
-                       float(beta_fast), float(beta_slow), out, ctypes.byref(amp))
+    st = fa_rope_freqs(rot_dim, float(base), ROPE_SCALING[scaling], float(factor), original_len, float(beta_fast),
+                       float(beta_slow), out, ctypes.byref(amp))
     if st != FA_OK:
         raise FAError(st, "fa_rope_freqs")
     return torch.tensor(list(out), dtype=torch.float64).to(device), amp.value
@@ -901,8 +910,8 @@ def decode_prefix(q, k_pages, v_pages, block_table, seq_lens, prefix_len: int, p
     them all (its other rows are not asked for them).  The shared rows
     are read once for the whole batch; a sequence shorter than ``prefix_len``
     sees those up to its length, whatever the others hold."""
-    return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, int(prefix_len), prefix_table, scale, out, lse,
-                         workspace, stream)
+    return _decode_pages(q, k_pages, v_pages, block_table, seq_lens, _c_int(prefix_len, "prefix_len"), prefix_table,
+                         scale, out, lse, workspace, stream)
 
 
 def check_device_error(stream=None):

@@ -147,3 +147,20 @@ def test_append_overlaps():
     one = pages(k=1 << 40, v=1 << 40)
     same = dict(k=rows(A, 0, 640, 64), v=rows(A, 0, 640, 64), pg=one)
     assert _hit(call(pg=one)) and _hit(call(**same)) and not _hit(call(**same, f=None))
+
+
+# ---------------------------------------------------------------- numbers that do not fit
+
+def test_numbers_beyond_32_bits_are_refused():
+    """2^32 + 4096 is not 4096."""
+    import torch
+    x, p = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    t, n = torch.zeros(1, 4, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    for big in ((1 << 32) + 64, 1 << 31, -(1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.decode_prefix(x, p, p, t, n, big)
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.rope_freqs(64, scaling="yarn", factor=4.0, original_len=big, device="cpu")
+    for big in ((1 << 32) + 64, 1 << 31):
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.rope_freqs(big, device="cpu")
