@@ -261,15 +261,20 @@ __device__ __forceinline__ void add_parts(RowSum<VEC>& sum, int n, int lane, L&&
     }
   }
 }
-// the finished row: O in 16 bits, LSE in natural units (a row of nothing: 0
-// and -inf; NaN scores give NaN)
+// the finished row: O in 16 bits, LSE of the sum w in natural units (a row of
+// nothing: 0 and -inf; NaN scores give NaN)
 template <int VEC, bool BF16>
-__device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int D, int lane, const RowSum<VEC>& r) {
+__device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int D, int lane, const RowSum<VEC>& r,
+                                          float w) {
   const float inv = r.w == 0.f ? 0.f : 1.f / r.w;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + VEC * lane);
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) dst[i] = pack2<BF16>(r.o[2 * i] * inv, r.o[2 * i + 1] * inv);
-  if (lane == 0) p.lse[row] = r.w == 0.f ? -INFINITY : (r.m + __log2f(r.w)) * 0.69314718055994531f;
+  if (lane == 0) p.lse[row] = w == 0.f ? -INFINITY : (r.m + __log2f(w)) * 0.69314718055994531f;
+}
+template <int VEC, bool BF16>
+__device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int D, int lane, const RowSum<VEC>& r) {
+  store_row<VEC, BF16>(p, row, D, lane, r, r.w);
 }
 
 // What beginning and ending a unit costs, in tiles.  Runs are cut at equal
@@ -421,8 +426,6 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
   // tiles of a sequence that is taken from row `start` on, and that row
   auto tiles_from = [&](int start, int end) { return max(1, (end - start + C::KT - 1) / C::KT); };
   auto start_of = [&](int end) { return !PRE || end >= behind ? behind : range_start(end, behind, p.n_pre); };
-  const int b_lo = (int)min((long long)threadIdx.x * chunk, (long long)p.B);
-  const int b_hi = threadIdx.x < FIND ? min(b_lo + chunk, p.B) : b_lo;
   long long total = 0;
   int most = 0;  // the largest cost of a sequence
   if (p.B <= FIND) {
@@ -895,8 +898,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NB>::THREADS, PagedCfg<D, NB>::CTA
         sum.w = 1.f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum.o[i] = u[i];
-        store_row<VEC, BF16>(p, q_row + r, D, lane, sum);
-        if (lane == 0) p.lse[q_row + r] = lt == 0.f ? -INFINITY : (mn + __log2f(lt)) * 0.69314718055994531f;
+        store_row<VEC, BF16>(p, q_row + r, D, lane, sum, lt);
       } else {
         const size_t slot = (size_t)(2 * sg.run + (begins ? 1 : 0)) * p.G + r;
         const bool whole = begins && ends;
