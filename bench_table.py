@@ -10,8 +10,8 @@ Device time with CUDA events on the launching stream, at least 3 warm-up
 calls, the mean of ``--iters`` calls, queued behind a ~10 ms spin so that the
 host's launch overhead never shows in a short call's events.  The forward/backward rows write a
 256 MiB buffer (above the 126 MB L2) between calls, outside the event pairs;
-the decode and paged rows alternate two input sets instead (each set's caches
-exceed L2).  FLOPs follow bench.py's convention (forward 4*S^2*D per head, halved
+the decode, paged and prefix rows go round over input sets instead, as many as
+it takes to hold twice what L2 holds (two at least).  FLOPs follow bench.py's convention (forward 4*S^2*D per head, halved
 under a causal mask; backward 2.5x that); decode counts the K and V cache
 bytes read once.
 """
@@ -48,6 +48,23 @@ DECODE = [  # (B, Hq, Hkv, L, D)
     (1, 32, 8, 32768, 128),
     (16, 16, 1, 8192, 64),
 ]
+
+
+L2_BYTES = 126 << 20
+
+
+def input_sets(nbytes: int) -> int:
+    """Sets of `nbytes` each that calls go round over, so that none finds its own in L2."""
+    return max(2, -(-2 * L2_BYTES // nbytes))
+
+
+def decode_bytes(B, Hkv, L, D) -> int:
+    return 4 * B * Hkv * L * D
+
+
+def prefix_bytes(B, Hkv, P, own, D) -> int:
+    """Shared rows once, and each sequence's own."""
+    return 4 * Hkv * D * (P + B * own)
 
 
 def flop_count(lengths, heads: int, d: int, causal: bool):
@@ -159,18 +176,18 @@ def main():
     if "decode" in parts:
         for B, Hq, Hkv, L, D in DECODE:
             sets = []
-            for seed in (42, 43):
+            for seed in range(42, 42 + input_sets(decode_bytes(B, Hkv, L, D))):
                 h = inputs.make_decode(B, Hq, Hkv, L, D, "bf16", seed=seed)
                 sets.append(tuple(h[x].to(dev) for x in ("q", "k", "v")))
             lens = torch.full((B,), L, dtype=torch.int32, device=dev)
-            nbytes = 2 * B * Hkv * L * D * 2
+            nbytes = decode_bytes(B, Hkv, L, D)
             for n in (fa.fa_decode_num_splits(B, Hkv, L), 0):
                 ws = torch.empty(max(1, fa.fa_decode_workspace_size(B, Hq, n, D)), device=dev, dtype=torch.uint8)
                 o = torch.empty_like(sets[0][0])
                 lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
 
                 def dec(i):
-                    q, k, v = sets[i % 2]
+                    q, k, v = sets[i % len(sets)]
                     fa.decode(q, k, v, lens, n_splits=n, out=o, lse=lse, workspace=ws)
 
                 t_d = timed(dec, max(args.iters, 30), do_flush=False)
@@ -182,7 +199,7 @@ def main():
             gen = torch.Generator(device=dev).manual_seed(42)
             n = L // page
             sets = []
-            for _ in range(2):
+            for _ in range(input_sets(decode_bytes(B, Hkv, L, D))):
                 pools = [torch.randn(B * n, Hkv, page, D, device=dev, generator=gen).to(torch.bfloat16)
                          for _ in range(2)]
                 table = torch.randperm(B * n, device=dev, generator=gen).to(torch.int32).view(B, n)
@@ -195,26 +212,30 @@ def main():
             ws = torch.empty(fa.fa_decode_paged_workspace_size(B, Hq, Hkv, D), device=dev, dtype=torch.uint8)
 
             def app(i):
-                kp, vp, table, q, k, v = sets[i % 2]
+                kp, vp, table, q, k, v = sets[i % len(sets)]
                 fa.append_paged(k, v, kp, vp, table, lens, q=q, freqs=freqs, amp=amp, q_out=rq)
 
             def dec(i):
-                kp, vp, table, *_ = sets[i % 2]
+                kp, vp, table, *_ = sets[i % len(sets)]
                 fa.decode_paged(rq, kp, vp, table, lens, out=o, lse=lse, workspace=ws)
 
             t_a, t_d = (timed(f, max(args.iters, 30), do_flush=False) for f in (app, dec))
             emit({"kind": "paged", "shape": f"B{B} Hq{Hq} Hkv{Hkv} L{L} D{D} page{page}", "dtype": "bf16",
-                  "append_us": t_a * 1e3, "decode_us": t_d * 1e3, "gbs": 4 * B * Hkv * L * D / t_d / 1e6})
+                  "append_us": t_a * 1e3, "decode_us": t_d * 1e3, "gbs": decode_bytes(B, Hkv, L, D) / t_d / 1e6})
             # the same batch behind one shared cache of this length, 64 rows each of their own
-            own = [torch.randn(B * n + B, Hkv, page, D, device=dev, generator=gen).to(torch.bfloat16) for _ in range(2)]
-            ids = torch.arange(B * n + B, device=dev, dtype=torch.int32)
-            both = torch.cat([ids[:n].expand(B, n), ids[B * n:, None]], 1).contiguous()
+            del sets
+            nbytes = prefix_bytes(B, Hkv, L, page, D)
+            sets = [[torch.randn(n + B, Hkv, page, D, device=dev, generator=gen).to(torch.bfloat16) for _ in range(2)]
+                    for _ in range(input_sets(nbytes))]
+            ids = torch.arange(n + B, device=dev, dtype=torch.int32)
+            both = torch.cat([ids[:n].expand(B, n), ids[n:, None]], 1).contiguous()
             longer = lens + page
             wp = torch.empty(fa.fa_decode_prefix_workspace_size(B, Hq, Hkv, L, D), device=dev, dtype=torch.uint8)
-            t_p = timed(lambda i: fa.decode_prefix(rq, *own, both, longer, L, out=o, lse=lse, workspace=wp),
-                        max(args.iters, 30), do_flush=False)
+            t_p = timed(lambda i: fa.decode_prefix(rq, *sets[i % len(sets)], both, longer, L, out=o, lse=lse,
+                                                   workspace=wp), max(args.iters, 30), do_flush=False)
             emit({"kind": "prefix", "shape": f"B{B} Hq{Hq} Hkv{Hkv} shared{L} own{page} D{D} page{page}",
-                  "dtype": "bf16", "us": t_p * 1e3, "tflops": 4 * B * Hq * (L + page) * D / t_p / 1e9})
+                  "dtype": "bf16", "us": t_p * 1e3, "gbs": nbytes / t_p / 1e6,
+                  "tflops": 4 * B * Hq * (L + page) * D / t_p / 1e9})
         for B, Hq, Hkv, S, D in ((1, 32, 32, 4096, 128), (4, 16, 16, 8192, 128)):
             sets = [[torch.randn(B, S, h, D, device=dev).to(torch.bfloat16).transpose(1, 2) for h in (Hq, Hkv)]
                     for _ in range(2)]
