@@ -302,8 +302,12 @@ int prefix_splits(long long units, int P) {
 // alone, reading them for each sequence, is done before prefix_kernel and the
 // join are: 4 sequences x 1024 rows x 8 heads of 128, 13 MB more: 11.5 against
 // 11.1 us on the GPU, but two launches instead of three (11.5 against 13.9 us
-// for the call); 32 x 1024, 130 MB: 20.5 against 16.0; 2 x 16384, 67 MB: 18.8
-// against 27.1; 4 x 16384: 27.8 against 27.6.
+// for the call); 32 x 1024, 130 MB: 20.5 against 16.0; 4 x 16384: 27.8 against
+// 27.6.  Two sequences, 8 heads of 128, read for each against a pass of their
+// own: 16384 rows 22.0 against 27.6 us, 32768 33.9 against 44.7, 131072 106
+// against 133; three: 4096 13.2 against 13.9, 16384 28.7 against 28.1.  Three
+// behind longer rows, which the second and third reading no longer find in L2,
+// are the rule's weak side: 32768 65.5 against 44.9 us, 131072 231 against 133.
 bool shared_pass(int B, int Hkv, int P, int D) {
   return P > 0 && B > 3 && (double)(B - 1) * P * Hkv * D * 4 > 24e6;
 }

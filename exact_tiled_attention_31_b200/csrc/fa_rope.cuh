@@ -106,11 +106,12 @@ __device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float (&c)[8
 }
 
 // n <= kRopeHeads rows of one token, xs and ys elements apart: turned by `pos`
-// (with sign -1 back) if `turn`, else copied.
-template <int D, bool BF16, bool INTER>
+// (with sign -1 back) if `turn`, else copied; zeros in their place if FILL and
+// `skip`.
+template <int D, bool BF16, bool INTER, bool FILL>
 __device__ __forceinline__ void rope_heads(const RopeItem<D, INTER>& item, const uint16_t* x, long long xs, uint16_t* y,
-                                           long long ys, int n, bool turn, const double* freqs, int pos, float amp,
-                                           float sign) {
+                                           long long ys, int n, bool turn, bool skip, const double* freqs, int pos,
+                                           float amp, float sign) {
   uint4 lo[kRopeHeads], hi[kRopeHeads];
 #pragma unroll
   for (int k = 0; k < kRopeHeads; ++k)
@@ -133,16 +134,11 @@ __device__ __forceinline__ void rope_heads(const RopeItem<D, INTER>& item, const
   for (int k = 0; k < kRopeHeads; ++k)
     if (k < n) {
       if (turn) rope_turn<BF16, INTER>(lo[k], hi[k], c, s);
+      if (FILL && skip) lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(y + item.lo) = lo[k];
       *reinterpret_cast<uint4*>(y + item.hi) = hi[k];
       y += ys;
     }
-}
-// n rows of one token, ys elements apart: zeros to two of its D / 8 chunks
-template <int D>
-__device__ __forceinline__ void zero_heads(int it, uint16_t* y, long long ys, int n) {
-  for (int k = 0; k < min(n, kRopeHeads); ++k, y += ys)
-    for (int c = 0; c < 2; ++c) reinterpret_cast<uint4*>(y)[2 * it + c] = make_uint4(0, 0, 0, 0);
 }
 // groups of kRopeHeads heads, none of them over two tensors
 __host__ __device__ constexpr int rope_groups(int heads) { return (heads + kRopeHeads - 1) / kRopeHeads; }
@@ -161,9 +157,9 @@ struct RopeParams {
   float sign;              // -1 turns back
 };
 
-// block: tokens x D / 16 items.  FILL: rows of no sequence become zero (an
-// instance of its own: as an argument it took q and k of 32 heads x 4096 rows
-// from 22.2 to 23.9 us)
+// block: tokens x D / 16 items.  FILL: rows of no sequence become zero, by the
+// same path as the others, in an instance of its own (q and k of 32 heads x 4096
+// packed rows 20.4 us either way; 23.0 with a branch that stores zeros).
 template <int D, bool BF16, bool INTER, bool FILL>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   pdl_wait();
@@ -175,19 +171,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   if (n >= (uint32_t)p.B * (uint32_t)p.S) return;
   const int b = n / (uint32_t)p.S, t = n - b * (uint32_t)p.S;
   int pos = t;
+  bool skip = false;
   if (p.cu) {
     const int s = seq_of(p.cu, p.nseq, t);
-    if (s < 0) {  // rows of no sequence stay as they were
-      if constexpr (FILL) {
-        const int first = rope_groups(p.heads[0]);
-        const bool w = group >= first;
-        const int h = (group - (w ? first : 0)) * kRopeHeads;
-        const RowsOut y = w ? p.y[1] : p.y[0];
-        zero_heads<D>(it, y.p + h * y.head + t * y.row, y.head, (w ? p.heads[1] : p.heads[0]) - h);
-      }
-      return;
-    }
-    pos = t - p.cu[s];
+    skip = s < 0;
+    if (!FILL && skip) return;  // rows of no sequence stay as they were
+    pos = t - p.cu[FILL ? max(s, 0) : s];
   }
   if (p.positions) pos = p.positions[b * p.pos_batch + t];
   const int first = rope_groups(p.heads[0]);
@@ -195,9 +184,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int h = (group - (w ? first : 0)) * kRopeHeads;
   const RowsIn x = w ? p.x[1] : p.x[0];
   const RowsOut y = w ? p.y[1] : p.y[0];
-  rope_heads<D, BF16, INTER>(RopeItem<D, INTER>(it, p.R), x.p + b * x.batch + h * x.head + t * x.row, x.head,
-                             y.p + b * y.batch + h * y.head + t * y.row, y.head, (w ? p.heads[1] : p.heads[0]) - h, true,
-                             p.freqs, pos, p.amp, p.sign);
+  rope_heads<D, BF16, INTER, FILL>(RopeItem<D, INTER>(it, p.R), x.p + b * x.batch + h * x.head + t * x.row, x.head,
+                                   y.p + b * y.batch + h * y.head + t * y.row, y.head,
+                                   (w ? p.heads[1] : p.heads[0]) - h, !skip, skip, p.freqs, pos, p.amp, p.sign);
 }
 
 // ---------------------------------------------------------------------------
@@ -251,33 +240,28 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendParams
   } else {
     i = p.seq_lens[b] - 1;
   }
-  if (i < 0) {
-    if constexpr (FILL) {
-      const int h = group * kRopeHeads;
-      if (h < p.Hq) zero_heads<D>(it, p.q_out.p + h * p.q_out.head + t * p.q_out.row, p.q_out.head, p.Hq - h);
-    }
-    return;
-  }
+  const bool skip = i < 0;
+  if (skip && (!FILL || group >= rope_groups(p.Hq))) return;
   const int pos = p.positions ? p.positions[t] : i;
   const int slot = i >> p.page_shift, row = i & ((1 << p.page_shift) - 1);
-  const int page = slot < p.max_pages ? p.table[b * p.table_stride + slot] : -1;
+  const int page = !(FILL && skip) && slot < p.max_pages ? p.table[b * p.table_stride + slot] : -1;
   const bool placed = page >= 0 && page < p.n_pages;
-  if (!placed && it == 0 && group == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
+  if (!placed && !(FILL && skip) && it == 0 && group == 0) record_error(DEV_ERR_ARG, APPEND_SITE_PAGE);
   // q's groups of heads, then k's, then v's
   const RopeItem<D, INTER> item(it, p.R);
   const int gq = rope_groups(p.Hq), gk = gq + rope_groups(p.Hkv);
   if (group < gq) {
     const int h = group * kRopeHeads;
-    rope_heads<D, BF16, INTER>(item, p.q.p + h * p.q.head + t * p.q.row, p.q.head,
-                               p.q_out.p + h * p.q_out.head + t * p.q_out.row, p.q_out.head, p.Hq - h, true, p.freqs,
-                               pos, p.amp, 1.f);
+    rope_heads<D, BF16, INTER, FILL>(item, p.q.p + h * p.q.head + t * p.q.row, p.q.head,
+                                     p.q_out.p + h * p.q_out.head + t * p.q_out.row, p.q_out.head, p.Hq - h, !skip, skip,
+                                     p.freqs, pos, p.amp, 1.f);
   } else if (placed) {
     const bool val = group >= gk;
     const int h = (group - (val ? gk : gq)) * kRopeHeads;
     const RowsIn x = val ? p.v : p.k;
     uint16_t* y = (val ? p.v_pages : p.k_pages) + page * p.page_stride + ((((long long)h << p.page_shift) + row) * D);
-    rope_heads<D, BF16, INTER>(item, x.p + h * x.head + t * x.row, x.head, y, (long long)D << p.page_shift, p.Hkv - h,
-                               !val, p.freqs, pos, p.amp, 1.f);
+    rope_heads<D, BF16, INTER, false>(item, x.p + h * x.head + t * x.row, x.head, y, (long long)D << p.page_shift,
+                                      p.Hkv - h, !val, false, p.freqs, pos, p.amp, 1.f);
   }
 }
 

@@ -444,8 +444,8 @@ fa_status fa_append_paged(const fa_rows* k, const fa_rows* v, const fa_rows* q, 
                           const double* freqs, int rot_dim, int interleaved, float amp, const int* positions, int D,
                           fa_dtype dt, void* stream);
 
-/* fa_append_paged for a q_out that holds nothing yet: the rows of tokens that
- * write nothing become zero in it. */
+/* fa_append_paged for a q_out that holds nothing yet: the rows of padding tokens
+ * and of tokens of no sequence become zero in it. */
 fa_status fa_append_paged_fill(const fa_rows* k, const fa_rows* v, const fa_rows* q, const fa_rows* q_out,
                                const fa_pages* pages, const int* seq_lens, const int* cu_seqlens, int nseq, int total,
                                const double* freqs, int rot_dim, int interleaved, float amp, const int* positions,
