@@ -306,3 +306,39 @@ def test_overlapping_outputs_are_refused(cuda_device):
     for x in (fused, other):
         assert all(torch.equal(a, b) for a, b in zip(parts(x), want))
     assert torch.equal(other[:, :, 10:], rest)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("where", ["first tile", "inside", "all shared rows"])
+def test_shared_rows_of_the_lowest_value_drop_out(cuda_device, dtype, where):
+    """Keys of the type's lowest value against queries that are all positive:
+    scores of -inf (bf16) or far below the others (fp16), in a pass of their own.
+    Their weight is zero, the rest exact; with nothing else O is 0 and LSE -inf (bf16)."""
+    dev, gen = cuda_device, torch.Generator().manual_seed(6)
+    lens = [P] * 20 + [P + 1 + 3 * i for i in range(60)]
+    kp, vp, table = make_cache(gen, lens, HKV, D, PAGE, dtype, shared=P // PAGE)
+    q = randn(gen, dtype, len(lens), HQ, D).abs() + 0.125
+    low = {"first tile": range(0, 128), "inside": range(130, 250), "all shared rows": range(P)}[where]
+    keep = [i for i in range(P) if i not in low]
+    for i in low:
+        kp[table[0, i // PAGE], :, i % PAGE] = torch.finfo(kp.dtype).min
+    o, lse = _prefix(dev, lens, kp, vp, table, q)
+    if not keep:  # the sequences of shared rows alone
+        if dtype == "bf16":
+            assert (o[:20] == 0).all() and torch.isneginf(lse[:20]).all()
+        else:
+            assert torch.isfinite(o[:20]).all() and torch.isfinite(lse[:20]).all()
+    first = 0 if keep else 20
+    G, k, v = HQ // HKV, f64(kp), f64(vp)
+    for b in range(first, len(lens)):
+        rows = keep + list(range(P, lens[b]))
+        kk, vv = (np.stack([x[table[b, i // PAGE], :, i % PAGE] for i in rows], 1).repeat(G, 0) for x in (k, v))
+        s = np.einsum("hnd,hd->hn", kk, f64(q)[b]) * D ** -0.5
+        e = np.exp(s - s.max(-1, keepdims=True))
+        w = e / e.sum(-1, keepdims=True)
+        e_s = ((D + 8) * 2.0 ** -24 + 2.0 ** -22) * np.einsum("hnd,hd->hn", np.abs(kk), f64(q)[b]).max(-1) * D ** -0.5
+        ref, mean_v = np.einsum("hn,hnd->hd", w, vv), np.einsum("hn,hnd->hd", w, np.abs(vv))
+        u = U[o.dtype]  # as in paged_helpers
+        tol = u * np.abs(ref) + 2.0 ** -25 + (2 * u + 2 * (2 * e_s[:, None] + 2.0 ** -21)) * mean_v
+        assert (np.abs(f64(o[b]) - ref) <= tol).all(), b
+        assert (np.abs(f64(lse[b]) - s.max(-1) - np.log(e.sum(-1))) <= 2 * e_s + 2.0 ** -20 + 1e-5).all(), b
