@@ -56,6 +56,13 @@ Stack stack_of(const void* data, long long run, std::initializer_list<std::pair<
   return s;
 }
 
+// Whether index * stride stays within 2^46 values, 2^47 bytes: no device's
+// addresses go further, and sums of it do not overflow.
+bool within(long long n, long long stride) { return n <= 1 || stride <= (1LL << 46) / (n - 1); }
+bool within(const fa_rows& r, int B, int S) {
+  return within(B, r.batch_stride) && within(r.heads, r.head_stride) && within(S, r.row_stride);
+}
+
 long long floor_div(long long a, long long b) { return a / b - (a % b != 0 && a < 0); }
 
 // Whether some run of a (from dimension i on, delta values behind b's start)
@@ -204,7 +211,8 @@ fa_status rope_call(const fa_rows* x, const fa_rows* y, int n, const double* fre
     return FA_ERR_INVALID_ARG;
   fa::RopeParams p = {};
   for (int i = 0; i < n; ++i) {
-    if (!rows_ok(&x[i]) || !rows_ok(&y[i]) || x[i].heads != y[i].heads) return FA_ERR_INVALID_ARG;
+    if (!rows_ok(&x[i]) || !rows_ok(&y[i]) || x[i].heads != y[i].heads || !within(x[i], B, S) || !within(y[i], B, S))
+      return FA_ERR_INVALID_ARG;
     p.x[i] = rows_in(x[i]);
     p.y[i] = rows_out(y[i]);
     p.heads[i] = x[i].heads;
@@ -254,6 +262,9 @@ fa_status append_call(const fa_rows* k, const fa_rows* v, const fa_rows* q, cons
   if ((long long)p.Hq + 2LL * pages->heads > 65535) return FA_ERR_UNSUPPORTED;
   // the pools apart from each other (one pool for both only where it takes the
   // same rows unrotated); q_out is q, in place, or apart from everything else
+  if (!within(pages->n_pages, pages->page_stride) || !within(*k, 1, total) || !within(*v, 1, total) ||
+      (q && (!within(*q, 1, total) || !within(*q_out, 1, total))))
+    return FA_ERR_INVALID_ARG;
   const long long page = (long long)pages->heads * pages->page_size * D;
   const Stack pool_k = stack_of(pages->k, page, {{pages->n_pages, pages->page_stride}});
   const Stack pool_v = stack_of(pages->v, page, {{pages->n_pages, pages->page_stride}});

@@ -164,3 +164,20 @@ def test_numbers_beyond_32_bits_are_refused():
     for big in ((1 << 32) + 64, 1 << 31):
         with pytest.raises(ValueError, match="32 bits"):
             fa.rope_freqs(big, device="cpu")
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="addresses that no launch may see")
+def test_strides_beyond_every_address_are_refused():
+    """Rows whose last index lies 2^47 bytes and more away, up to strides whose sums pass 64 bits."""
+    far = (1 << 47, 1 << 60, (1 << 63) - 8)
+    for s in far:
+        for r in (rows(A, s, 640, 64), rows(A, 4096, s, 64), rows(A, 4096, 640, s)):
+            other = rows(A + (1 << 30), 4096, 640, 64)
+            assert _hit(_rope((r,), (other,), 2, 10)) and _hit(_rope((other,), (r,), 2, 10))
+        for bad in (dict(k=rows(A, 0, s, 64)), dict(v=rows(A, 0, 640, s)), dict(q=rows(A, 0, s, 64), qo=rows(A, 0, s, 64))):
+            a = {**dict(k=rows(), v=rows(A + (1 << 20)), q=None, qo=None), **bad}
+            assert _hit(lambda: fa.fa_append_paged(a["k"], a["v"], a["q"], a["qo"], pages(k=1 << 40, v=1 << 41), A, None, 10,
+                                                   10, A, 64, 0, 1.0, None, 64, 0, None)), (s, bad)
+    assert _hit(lambda: fa.fa_append_paged(rows(), rows(A + (1 << 20)), None, None, pages(stride=1 << 38, n=(1 << 31) - 1), A,
+                                           None, 10, 10, A, 64, 0, 1.0, None, 64, 0, None))
+    assert not _hit(_rope((rows(A, 1 << 40, 640, 64),), (rows(A + (1 << 30), 1 << 40, 640, 64),), 2, 10))
