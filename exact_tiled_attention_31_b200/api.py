@@ -595,23 +595,35 @@ def _row_strides(shape, strides, dims, out=False):
 
 def _rows_layout(x, y, order):
     """Of rows x and where they go, y (None: a new contiguous tensor): what
-    fa_rows says behind the pointer, for both, and what _apart needs.
-    ``order``: the dimensions of batch (or None), heads and tokens."""
+    fa_rows says behind the pointer, for both.  ``order``: the dimensions of
+    batch (or None), heads and tokens."""
     if y is not None and (y.shape != x.shape or y.dtype != x.dtype):
         raise ValueError(f"output {tuple(y.shape)} {y.dtype} does not match {tuple(x.shape)} {x.dtype}")
-    heads, said, size = x.shape[order[1]], [], []
+    heads, said = x.shape[order[1]], []
     for st, out in ((x.stride(), False), (_contiguous(x.shape) if y is None else y.stride(), True)):
         s = _row_strides(x.shape, st, [d for d in order if d is not None], out)
         said.append((*(s if order[0] is not None else (0, *s)), heads))
-        size.append(2 * (1 + sum((n - 1) * k for n, k in zip(x.shape, st))) if x.numel() else 0)
-    return (*said, *size, y is not None and y.stride() == x.stride())
+    return said
 
 
-def _apart(x, y, layout):
-    """An output is its input, in place, or apart from it."""
-    _, _, nx, ny, same = layout
-    if not (same and x == y) and x < y + ny and y < x + nx:
-        raise ValueError("an output overlaps its input without being it")
+def _refused(status, what, pairs, others=()):
+    """Raise for a status that is not FA_OK, of a call with these (output,
+    input) pairs.  The C entries decide whether outputs overlap anything (views
+    of one buffer may lie between one another); where they refuse a call whose
+    outputs reach into another tensor, say so."""
+    def span(t):
+        at = t.data_ptr()
+        return at, at + t.element_size() * (1 + sum((n - 1) * k for n, k in zip(t.shape, t.stride())))
+    if status == FA_ERR_INVALID_ARG:
+        for i, (y, x) in enumerate(pairs):
+            rest = [o for o, _ in pairs[:i]] + [z for j, (_, z) in enumerate(pairs) if j != i] + list(others)
+            if y.data_ptr() != x.data_ptr() or y.stride() != x.stride():
+                rest.append(x)
+            for z in rest:
+                (c, d), (e, f) = span(y), span(z)
+                if y.numel() and z.numel() and c < f and e < d:
+                    raise ValueError(f"{what}: an output overlaps another tensor of the call, other than its input in place")
+    raise FAError(status, what)
 
 
 def _check_freqs(freqs):
@@ -694,22 +706,16 @@ def _rope_call(raw, known, q, k, freqs, positions, cu_seqlens, interleaved, amp,
             yk = _torch.empty(k.shape, dtype=k.dtype, device=k.device)
     xp, yp = q.data_ptr(), yq.data_ptr()
     x, y = _ROWS.pack(xp, *rows[0][0]), _ROWS.pack(yp, *rows[0][1])
-    if given:
-        _apart(xp, yp, rows[0])
     if k is not None:
         kp, ykp = k.data_ptr(), yk.data_ptr()
         x += _ROWS.pack(kp, *rows[1][0])
         y += _ROWS.pack(ykp, *rows[1][1])
-        if given:
-            _apart(kp, ykp, rows[1])
-            if ykp == yp and ykp:
-                raise ValueError("the two outputs are the same memory")
     if not empty:
         call = _lib.fa_rope if given else _lib.fa_rope_fill
         st = call(x, y, len(rows), freqs.data_ptr(), rot, interleaved, amp, backward, _ptr(positions), pos_stride,
                   _ptr(cu_seqlens), nseq, B, S, D, dt, raw)
         if st != FA_OK:
-            raise FAError(st, "fa_rope")
+            _refused(st, "fa_rope", [p for p in ((yq, q), (yk, k)) if given and p[0] is not None])
     return yq, yk
 
 
@@ -821,8 +827,6 @@ def _append_call(raw, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_s
         if q_out is None:
             to = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
         xp, yp = q.data_ptr(), to.data_ptr()
-        if q_out is not None:
-            _apart(xp, yp, q_rows)
         qx, qy = _ROWS.pack(xp, *q_rows[0]), _ROWS.pack(yp, *q_rows[1])
     if T:
         call = _lib.fa_append_paged_fill if q_out is None else _lib.fa_append_paged
@@ -830,7 +834,7 @@ def _append_call(raw, known, k, v, k_pages, v_pages, block_table, seq_lens, cu_s
                   _pack_pages(k_pages, v_pages, block_table, pages), seq_lens.data_ptr(), _ptr(cu_seqlens), B, T,
                   _ptr(freqs), rot, interleaved, amp, _ptr(positions), D, dt, raw)
         if st != FA_OK:
-            raise FAError(st, "fa_append_paged")
+            _refused(st, "fa_append_paged", [] if q_out is None else [(q_out, q)], (k, v, k_pages, v_pages))
     return to
 
 

@@ -342,3 +342,24 @@ def test_shared_rows_of_the_lowest_value_drop_out(cuda_device, dtype, where):
         tol = u * np.abs(ref) + 2.0 ** -25 + (2 * u + 2 * (2 * e_s[:, None] + 2.0 ** -21)) * mean_v
         assert (np.abs(f64(o[b]) - ref) <= tol).all(), b
         assert (np.abs(f64(lse[b]) - s.max(-1) - np.log(e.sum(-1))) <= 2 * e_s + 2.0 ** -20 + 1e-5).all(), b
+
+
+def test_outputs_between_the_rows_of_their_inputs(cuda_device):
+    """An output in another place of its input's buffer, its rows between the input's."""
+    bf = dict(dtype=torch.bfloat16, device=cuda_device)
+    f = torch.from_numpy(freqs_of(64)).to(cuda_device)
+    buf = torch.randn(2, 6, 16, 64, **bf).transpose(1, 2)
+    q, k, rest = buf[:, :4], buf[:, 4:6], buf[:, 12:].clone()
+    want = fa.rope(q, k, f)
+    got = fa.rope(q, k, f, out=(buf[:, 6:10], buf[:, 10:12]))
+    one = torch.randn(3, 12, 64, **bf)
+    kp, vp = (torch.zeros(3, 2, 16, 64, **bf) for _ in range(2))
+    args = (kp, vp, _i32([[0], [1], [2]], cuda_device), _i32([5, 6, 7], cuda_device))
+    want1 = fa.append_paged(one[:, 4:6], one[:, 6:8], *args, q=one[:, :4], freqs=f)
+    got1 = fa.append_paged(one[:, 4:6], one[:, 6:8], *args, q=one[:, :4], freqs=f, q_out=one[:, 8:])
+    fa.check_device_error()
+    assert all(torch.equal(a, b) for a, b in zip((*got, got1), (*want, want1))) and torch.equal(buf[:, 12:], rest)
+    for call in (lambda: fa.rope(q, k, f, out=(k.repeat(1, 2, 1, 1), buf[:, 5:7])),
+                 lambda: fa.append_paged(one[:, 4:6], one[:, 6:8], *args, q=one[:, :4], freqs=f, q_out=one[:, 3:7])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
