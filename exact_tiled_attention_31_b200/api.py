@@ -725,9 +725,10 @@ def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved: bool = False
     tensors, or packed [H, T, D] ones with ``cu_seqlens``.  Inputs may be any
     views whose rows are contiguous (a transposed projection, say); the
     outputs are contiguous, or ``out`` = (q_out, k_out), which may be the
-    inputs themselves but not overlap anything of the call otherwise.  Rows behind the last sequence are zero in new outputs
-    and left as they were in ``out``.  ``freqs`` and ``amp`` come from ``rope_freqs``;
-    ``positions`` (int32 [S] or [B, S]; packed [T]) defaults to the index in
+    inputs themselves but not overlap anything else of the call.  Rows behind
+    the last sequence are zero in new outputs and left as they were in
+    ``out``.  ``freqs`` and ``amp`` come from ``rope_freqs``; ``positions``
+    (int32 [S] or [B, S]; packed [T]) defaults to the index in
     the sequence.  The columns past the rotated ones are copied."""
     return _rope(q, k, freqs, positions, cu_seqlens, interleaved, amp, out, stream, False)
 
